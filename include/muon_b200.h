@@ -201,6 +201,91 @@ muon_status readout_blend(const void* theta, int32_t theta_dtype, const float* e
                           void* out, int32_t out_dtype, int64_t n, float w_final,
                           void* stream);
 
+/* ---------------------------------------------------------------- 4 bits
+ * Products, quantisation and dropout around the step: a layer's forward and
+ * backward products read the parameters a step wrote and make the gradient
+ * the next one reads.
+ *
+ * MXFP4: e2m1 elements {0, .5, 1, 1.5, 2, 3, 4, 6} and their negatives, and
+ * one power-of-two scale per 32 of them along the last axis. A matrix
+ * [rows][cols] with blocks = ceil(cols / 32) is stored as
+ *   data   [count][rows][blocks * 16] bytes, two elements per byte, the first
+ *          in the low half; elements past cols are zero;
+ *   scales [count][ceil(rows / 128)][ceil(blocks / 4)][512] bytes: exponent +
+ *          127 (255: the block stands for NaN) of row r, block b of a 128 x 4
+ *          tile at (r % 32) * 16 + (r / 32) * 4 + b; the padding is zero.
+ * Sizes: count, rows, cols >= 1; rows and cols below 2^24; count * rows,
+ * count * cols, count times the 128 x 128 tiles, and for the read-back and
+ * dropout the number of 8-column groups, below 2^31 (MUON_ERR_SHAPE).
+ *
+ * Random numbers (dropout, stochastic rounding) come from Philox4x32-10, so
+ * that nothing is stored and a backward pass forms them again. rng points to
+ * two int64 in device memory, (seed, offset), read when the work runs: a
+ * captured graph draws new numbers if the caller advances the offset between
+ * replays. With n = (offset + site) mod 2^64, element (r, c) of matrix m
+ * (row m * rows + r) takes half (c & 1) of word (c >> 1) & 3 under key = seed and
+ * counter (c >> 3, m * rows + r, lo32(n), (hi32(n) & 0x3fffffff) | d << 30),
+ * d = 0 for dropout, 1 for the rounding of out, 2 for the rounding of out_t
+ * (whose rows are the source's columns). site tells the calls of one step
+ * apart. */
+typedef struct {
+  int64_t count, rows, cols;
+  void* data;               /* device, muon_mxfp4_data_size bytes   */
+  void* scales;             /* device, muon_mxfp4_scales_size bytes */
+} muon_mxfp4;
+
+/* Bytes of the two buffers (host only; 0 if the sizes are invalid). */
+size_t muon_mxfp4_data_size(int64_t count, int64_t rows, int64_t cols);
+size_t muon_mxfp4_scales_size(int64_t count, int64_t rows, int64_t cols);
+
+/* out = [residual +] dropout(x): with t = the multiple of 2^-16 nearest to p,
+ * an element whose 16-bit number is below t 2^16 becomes 0 and the others are
+ * multiplied by 1 / (1 - t). x, residual (NULL: none) and out: device
+ * [rows][cols] of one dtype; out may be x or residual itself, and must not
+ * overlap them otherwise. 0 <= p, t < 1. The gradient's pass is the same call
+ * on the output's gradient. */
+muon_status muon_dropout(const void* x, const void* residual, void* out, int32_t dtype, int64_t rows,
+                         int64_t cols, double p, const int64_t* rng, uint64_t site, void* stream);
+
+/* Quantises x, device [count][rows][cols]: out gets blocks along the columns
+ * (count, rows, cols as x), out_t the transposed matrices with blocks along
+ * x's rows (count, cols, rows); either may be NULL, and both are written from
+ * one read of x. The scale is the smallest power of two (at least 2^-127) with
+ * amax / scale <= 6, so nothing saturates. stochastic = 0 rounds to nearest,
+ * ties to the even code; 1 rounds to one of the two neighbours with the
+ * probabilities that keep the mean, out and out_t independently. p > 0 first
+ * applies muon_dropout's mask and factor (x as [count * rows][cols]). rng is
+ * needed for p > 0 and for stochastic rounding, else NULL. A block with an
+ * infinity or a NaN stands for NaN. */
+muon_status muon_mxfp4_quantize(const void* x, int32_t dtype, int64_t count, int64_t rows,
+                                int64_t cols, const muon_mxfp4* out, const muon_mxfp4* out_t, double p,
+                                int32_t stochastic, const int64_t* rng, uint64_t site, void* stream);
+
+/* Quantises readout_blend's result, w_final theta + (1 - w_final) ema (to
+ * nearest), without storing it: theta [count][rows][cols] of dtype, ema fp32. */
+muon_status muon_mxfp4_readout(const void* theta, int32_t dtype, const float* ema, float w_final,
+                               int64_t count, int64_t rows, int64_t cols, const muon_mxfp4* out,
+                               const muon_mxfp4* out_t, void* stream);
+
+/* Reads back: out = the values of q, device [count][rows][cols] of dtype
+ * (exact in either dtype, but for 2^128 and above, which become infinity). */
+muon_status muon_mxfp4_dequantize(const muon_mxfp4* q, void* out, int32_t dtype, void* stream);
+
+/* Bytes of workspace muon_mxfp4_matmul needs for these sizes (host only; 0 if
+ * they are invalid): the status word, and the partial sums of products that
+ * are split along k. Zero-fill a new workspace once. Calls that may overlap on
+ * the device need workspaces of their own. */
+size_t muon_mxfp4_matmul_workspace_size(int64_t count, int64_t m, int64_t n, int64_t k);
+
+/* out = [add +] a b^T per matrix: a (count, m, k), b (count, n, k), out and add
+ * (NULL: none) device [count][m][n] of out_dtype. a or b may have one matrix
+ * (count 1) that serves every product. fp32 accumulation, one rounding. out
+ * may be add itself; it must not overlap add otherwise, nor a, b or the
+ * workspace. A device-side wait that ran out is recorded in ws's status word
+ * (muon_device_status); out is then incomplete. */
+muon_status muon_mxfp4_matmul(const muon_mxfp4* a, const muon_mxfp4* b, const void* add, void* out,
+                              int32_t out_dtype, void* ws, size_t ws_bytes, void* stream);
+
 /* Synchronises `stream`, then reads the workspace's device status word:
  * MUON_OK, or MUON_ERR_TIMEOUT if a bounded wait inside a kernel ran out
  * since the word was last cleared. clear != 0 resets it to MUON_OK. This

@@ -40,7 +40,10 @@ STATUS_NAMES = {
 EXPORTED = ("muon_abi_version", "muon_status_string", "muon_workspace_size", "muon_step",
             "anvil_step", "muon_orthogonalize", "ema_update", "readout_blend",
             "muon_device_status", "muon_set_debug", "muon_set_ns_events",
-            "muon_orthogonalize_static", "muon_chain_plan")
+            "muon_orthogonalize_static", "muon_chain_plan",
+            "muon_dropout", "muon_mxfp4_data_size", "muon_mxfp4_scales_size", "muon_mxfp4_quantize",
+            "muon_mxfp4_readout", "muon_mxfp4_dequantize", "muon_mxfp4_matmul_workspace_size",
+            "muon_mxfp4_matmul")
 
 
 class MuonError(RuntimeError):
@@ -66,6 +69,11 @@ class CHparams(ctypes.Structure):
                 ("sgd_momentum", ctypes.c_int32)]
 
 
+class CMxfp4(ctypes.Structure):
+    _fields_ = [("count", ctypes.c_int64), ("rows", ctypes.c_int64), ("cols", ctypes.c_int64),
+                ("data", ctypes.c_void_p), ("scales", ctypes.c_void_p)]
+
+
 _vp, _i32, _i64, _sz, _f = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float
 _sig = {
     "muon_abi_version": (_i32, []),
@@ -83,6 +91,17 @@ _sig = {
     "muon_chain_plan": (_i64, [ctypes.POINTER(_i64), _i32, _i32, ctypes.POINTER(_i32), _i64]),
     "muon_orthogonalize_static": (_i32, [_vp, _i32, _vp, _i32, _i64, _i64, _i64,
                                          ctypes.POINTER(CHparams), _vp]),
+    "muon_dropout": (_i32, [_vp, _vp, _vp, _i32, _i64, _i64, ctypes.c_double, _vp, ctypes.c_uint64, _vp]),
+    "muon_mxfp4_data_size": (_sz, [_i64, _i64, _i64]),
+    "muon_mxfp4_scales_size": (_sz, [_i64, _i64, _i64]),
+    "muon_mxfp4_quantize": (_i32, [_vp, _i32, _i64, _i64, _i64, ctypes.POINTER(CMxfp4),
+                                   ctypes.POINTER(CMxfp4), ctypes.c_double, _i32, _vp, ctypes.c_uint64, _vp]),
+    "muon_mxfp4_readout": (_i32, [_vp, _i32, _vp, _f, _i64, _i64, _i64, ctypes.POINTER(CMxfp4),
+                                  ctypes.POINTER(CMxfp4), _vp]),
+    "muon_mxfp4_dequantize": (_i32, [ctypes.POINTER(CMxfp4), _vp, _i32, _vp]),
+    "muon_mxfp4_matmul_workspace_size": (_sz, [_i64, _i64, _i64, _i64]),
+    "muon_mxfp4_matmul": (_i32, [ctypes.POINTER(CMxfp4), ctypes.POINTER(CMxfp4), _vp, _vp, _i32, _vp, _sz,
+                                 _vp]),
 }
 for _name, (_res, _args) in _sig.items():
     _fn = getattr(_lib, _name)
@@ -271,6 +290,174 @@ def readout_blend(theta, ema, out, w_final: float = 0.35, stream=None) -> None:
            "readout_blend")
 
 
+# ------------------------------------------------------- dropout and 4 bits
+@dataclass
+class Mxfp4:
+    """Matrices [count, rows, cols] in microscaled 4-bit floating point, blocks
+    of 32 along cols. data: the codes, scales: one byte per block in tiles of
+    128 rows x 4 blocks (both uint8; the header describes the layout)."""
+    data: "object"
+    scales: "object"
+    shape: Tuple[int, int, int]
+
+
+def _shape3(shape) -> Tuple[int, int, int]:
+    s = tuple(int(v) for v in shape)
+    if len(s) == 2:
+        s = (1,) + s
+    if len(s) != 3:
+        raise ValueError("expected (rows, cols) or (count, rows, cols)")
+    return s  # type: ignore[return-value]
+
+
+def alloc_mxfp4(shape, device="cuda") -> Mxfp4:
+    """Storage for matrices (count, rows, cols) or (rows, cols) in 4 bits."""
+    import torch
+    c, r, k = _shape3(shape)
+    n = int(_lib.muon_mxfp4_data_size(c, r, k))
+    if n == 0:
+        raise MuonError(2, "alloc_mxfp4")
+    data = torch.empty((c, r, n // (c * r)), dtype=torch.uint8, device=device)
+    scales = torch.empty((c, -(-r // 128), -(-k // 128), 512), dtype=torch.uint8, device=device)
+    return Mxfp4(data, scales, (c, r, k))
+
+
+def _cmx(q: Optional[Mxfp4], what: str):
+    if q is None:
+        return None
+    import torch
+    c, r, k = _shape3(q.shape)
+    n, m = _lib.muon_mxfp4_data_size(c, r, k), _lib.muon_mxfp4_scales_size(c, r, k)
+    if q.data.dtype != torch.uint8 or q.scales.dtype != torch.uint8:
+        raise ValueError(f"{what}: data and scales must be uint8")
+    if n and (q.data.numel() != n or q.scales.numel() != m):
+        raise ValueError(f"{what}: storage of {q.data.numel()} + {q.scales.numel()} bytes for {n} + {m}")
+    return CMxfp4(c, r, k, _ptr(q.data), _ptr(q.scales))
+
+
+class _Launch:
+    """The device that a call's tensors share, made current for the call, and
+    the stream it runs on (the device's current one unless given)."""
+
+    def __init__(self, tensors, stream):
+        import torch
+        devices = {t.device for t in tensors if t is not None}
+        if len(devices) != 1 or next(iter(devices)).type != "cuda":
+            raise ValueError("the tensors of a call must be on one CUDA device")
+        self._guard = None
+        dev = next(iter(devices))
+        if dev.index != torch.cuda.current_device():
+            self._guard = torch.cuda.device(dev)
+        self._stream = stream
+
+    def __enter__(self):
+        if self._guard is not None:
+            self._guard.__enter__()
+        return _stream_handle(self._stream)
+
+    def __exit__(self, *exc):
+        if self._guard is not None:
+            self._guard.__exit__(*exc)
+
+
+def _check_rng(rng) -> None:
+    import torch
+    if rng is not None and (rng.dtype != torch.int64 or rng.numel() != 2):
+        raise ValueError("rng must be two int64: (seed, offset)")
+
+
+def dropout(x, out, p: float, rng, site: int = 0, residual=None, stream=None) -> None:
+    """out = [residual +] dropout(x): elements are dropped with probability p
+    (to the nearest 2^-16), the others scaled by 1 / (1 - p). x: [..., cols],
+    bf16 or fp32; out may be x or residual. rng: int64 (seed, offset) on the
+    device, site: the call's place within the step. The mask depends on them,
+    the row and the column only; the gradient's pass is the same call on the
+    output's gradient."""
+    _check_rng(rng)
+    for t, name in ((out, "out"), (residual, "residual")):
+        if t is not None and (t.shape != x.shape or t.dtype != x.dtype):
+            raise ValueError(f"{name} must have x's shape and dtype")
+    cols = x.shape[-1] if x.dim() else 1
+    rows = x.numel() // cols if cols else 0
+    with _Launch((x, out, rng, residual), stream) as s:
+        _check(_lib.muon_dropout(_ptr(x), _ptr(residual), _ptr(out), _dtype_code(x), rows, cols, p, _ptr(rng),
+                                 site, s), "dropout")
+
+
+def mxfp4_quantize(x, out: Optional[Mxfp4] = None, out_t: Optional[Mxfp4] = None, dropout: float = 0.0,
+                   stochastic: bool = False, rng=None, site: int = 0, stream=None) -> None:
+    """Quantises x ([count, rows, cols] or [rows, cols], bf16 or fp32) into out
+    (blocks along cols), and its transpose into out_t (blocks along rows), from
+    one read. dropout > 0 first applies dropout()'s mask and factor (of the
+    same rng and site, x seen as [count * rows, cols]); stochastic rounds
+    without bias, out and out_t independently. A block with an infinity or a
+    NaN stands for NaN."""
+    _check_rng(rng)
+    c, r, k = _shape3(x.shape)
+    q, qt = _cmx(out, "out"), _cmx(out_t, "out_t")
+    tensors = [x, rng] + [t for m in (out, out_t) if m is not None for t in (m.data, m.scales)]
+    with _Launch(tensors, stream) as s:
+        _check(_lib.muon_mxfp4_quantize(_ptr(x), _dtype_code(x), c, r, k, q, qt, dropout, 1 if stochastic else 0,
+                                        _ptr(rng), site, s), "mxfp4_quantize")
+
+
+def mxfp4_readout(theta, ema, out: Optional[Mxfp4] = None, out_t: Optional[Mxfp4] = None,
+                  w_final: float = 0.35, stream=None) -> None:
+    """Quantises the readout blend w_final theta + (1 - w_final) ema without
+    storing it: the codes of readout_blend's fp32 result."""
+    if ema.shape != theta.shape or _dtype_code(ema) != F32:
+        raise ValueError("ema must be float32 of theta's shape")
+    c, r, k = _shape3(theta.shape)
+    q, qt = _cmx(out, "out"), _cmx(out_t, "out_t")
+    tensors = [theta, ema] + [t for m in (out, out_t) if m is not None for t in (m.data, m.scales)]
+    with _Launch(tensors, stream) as s:
+        _check(_lib.muon_mxfp4_readout(_ptr(theta), _dtype_code(theta), _ptr(ema), w_final, c, r, k, q, qt, s),
+               "mxfp4_readout")
+
+
+def mxfp4_dequantize(q: Mxfp4, out, stream=None) -> None:
+    """out ([count, rows, cols] or [rows, cols], bf16 or fp32) = the values of
+    q, exactly (2^128 and above become infinity)."""
+    cq = _cmx(q, "q")
+    if _shape3(out.shape) != _shape3(q.shape):
+        raise ValueError("out must have q's shape")
+    with _Launch((q.data, q.scales, out), stream) as s:
+        _check(_lib.muon_mxfp4_dequantize(cq, _ptr(out), _dtype_code(out), s), "mxfp4_dequantize")
+
+
+def matmul_workspace_size(a_shape, b_shape) -> int:
+    """Bytes of workspace for mxfp4_matmul of (count, m, k) and (count, n, k)."""
+    (ca, m, k), (cb, n, kb) = _shape3(a_shape), _shape3(b_shape)
+    if k != kb or (ca != cb and 1 not in (ca, cb)):
+        return 0
+    return int(_lib.muon_mxfp4_matmul_workspace_size(max(ca, cb), m, n, k))
+
+
+def alloc_matmul_workspace(a_shape, b_shape, device="cuda"):
+    """A zero-filled uint8 workspace for mxfp4_matmul of these shapes."""
+    import torch
+    n = matmul_workspace_size(a_shape, b_shape)
+    if n == 0:
+        raise MuonError(2, "matmul_workspace_size")
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def mxfp4_matmul(a: Mxfp4, b: Mxfp4, out, workspace, add=None, stream=None) -> None:
+    """out = [add +] a b^T: a (count, m, k), b (count, n, k), out and add
+    [count, m, n] in bf16 or fp32 (out may be add). a or b with count 1 serves
+    every product. Accumulates in fp32 and rounds once. The workspace may not
+    be shared by calls that overlap on the device; device_status(workspace)
+    reports a device-side wait that ran out."""
+    ca, cb = _cmx(a, "a"), _cmx(b, "b")
+    if _shape3(out.shape) != (max(ca.count, cb.count), ca.rows, cb.rows):
+        raise ValueError("out must be [count, a's rows, b's rows]")
+    if add is not None and (add.shape != out.shape or add.dtype != out.dtype):
+        raise ValueError("add must have out's shape and dtype")
+    with _Launch((a.data, a.scales, b.data, b.scales, out, workspace, add), stream) as s:
+        _check(_lib.muon_mxfp4_matmul(ca, cb, _ptr(add), _ptr(out), _dtype_code(out), _ptr(workspace),
+                                      workspace.numel() * workspace.element_size(), s), "mxfp4_matmul")
+
+
 def device_status(workspace, stream=None, clear: bool = False) -> int:
     """Synchronises the stream and returns the workspace's device status code."""
     return int(_lib.muon_device_status(_ptr(workspace), workspace.numel() * workspace.element_size(),
@@ -301,5 +488,8 @@ def loaded_library_path() -> str:
 __all__: List[str] = ["Bank", "Hparams", "MuonError", "workspace_size", "alloc_workspace",
                       "muon_step", "anvil_step", "orthogonalize", "ema_update", "readout_blend",
                       "checkpoint_average_betas",
+                      "Mxfp4", "alloc_mxfp4", "dropout", "mxfp4_quantize", "mxfp4_readout",
+                      "mxfp4_dequantize", "mxfp4_matmul", "matmul_workspace_size",
+                      "alloc_matmul_workspace", "CMxfp4",
                       "device_status", "set_debug", "set_ns_events", "status_string", "abi_version",
                       "raw_library", "CBank", "CHparams", "EXPORTED", "F32", "BF16"]

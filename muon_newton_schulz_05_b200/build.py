@@ -20,8 +20,10 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libmuonb200.so")
 LIB_CHECK = os.path.join(PKG, "libmuonb200_check.so")
-SOURCES = ["api.cu", "elementwise.cu", "ns_gemm.cu"]
-HEADERS = ["plan.cuh", "ptx.cuh", "tiles.cuh", "update_math.cuh", "check.cuh"]
+SOURCES = ["api.cu", "elementwise.cu", "ns_gemm.cu", "lowbit_api.cu", "dropout.cu", "mxfp4_quant.cu",
+           "mxfp4_gemm.cu"]
+HEADERS = ["plan.cuh", "ptx.cuh", "tiles.cuh", "update_math.cuh", "check.cuh", "lowbit.cuh", "philox.cuh",
+           "dtype_io.cuh", "mxfp4_gemm.cuh", "ptx_mxf4.cuh"]
 
 
 def nvcc() -> str:

@@ -10,6 +10,7 @@
 #include <utility>
 
 #include "muon_b200.h"
+#include "lowbit.cuh"
 #include "plan.cuh"
 #include "tiles.cuh"
 
@@ -59,6 +60,26 @@ muon_status device_state(int* sms, int* max_pairs = nullptr) {
   if (max_pairs) *max_pairs = d.max_pairs;
   return MUON_OK;
 }
+
+}  // namespace
+
+namespace muon {
+muon_status library_device(int* sms) { return device_state(sms); }
+
+double wait_limit_seconds() { return g_debug.wait_limit_s > 0 ? g_debug.wait_limit_s : 2.0; }
+
+muon_status encode_tiled(CUtensorMap* m, CUtensorMapDataType type, int rank, const void* ptr,
+                         const cuuint64_t* dims, const cuuint64_t* strides, const cuuint32_t* box,
+                         CUtensorMapSwizzle swz) {
+  const cuuint32_t one[3] = {1, 1, 1};
+  const CUresult r = g_encode(m, type, rank, const_cast<void*>(ptr), dims, strides, box, one,
+                              CU_TENSOR_MAP_INTERLEAVE_NONE, swz, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? MUON_OK : MUON_ERR_CUDA;
+}
+}  // namespace muon
+
+namespace {
 
 // ------------------------------------------------------------ validation
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }

@@ -1,0 +1,96 @@
+// Dropout from a counter-based generator: out = [residual +] x k / (1 - t / 2^16),
+// k = 1 where the element's 16-bit number is at least t. The mask is never
+// stored; the backward pass is the same call on the output's gradient.
+// p is taken to the nearest multiple t of 2^-16 and the scale belongs to that
+// t, so the expectation is exact.
+#include "dtype_io.cuh"
+#include "lowbit.cuh"
+#include "philox.cuh"
+
+namespace muon {
+
+__device__ __forceinline__ float dropped(float x, uint32_t u16, uint32_t threshold, float scale) {
+  return u16 >= threshold ? x * scale : 0.0f;
+}
+
+__device__ __forceinline__ uint32_t half_of(const uint4& w, int j) {
+  const uint32_t v = j < 2 ? w.x : j < 4 ? w.y : j < 6 ? w.z : w.w;
+  return (j & 1) ? v >> 16 : v & 0xFFFFu;
+}
+
+// Rows whose length is a multiple of 8: one group of 8 columns, one Philox
+// call, per thread.
+template <bool kBf16, bool kResidual>
+__global__ void __launch_bounds__(256) dropout_kernel(const __grid_constant__ DropoutParams p) {
+  const RngKey key = rng_key(p.rng, p.site);
+  const uint32_t step = gridDim.x * 256u;
+  for (uint32_t i = blockIdx.x * 256u + threadIdx.x; i < p.total; i += step) {
+    const int row = fdiv(static_cast<int>(i), p.fd_groups);
+    const int g = static_cast<int>(i) - row * p.groups;
+    const long long at = static_cast<long long>(i) * 8;
+    float x[8], r[8];
+    load8t<kBf16>(p.x, at, x);
+    if (kResidual) load8t<kBf16>(p.residual, at, r);
+    const uint4 u = philox8(key, kRngDropout, static_cast<uint32_t>(row), static_cast<uint32_t>(g));
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      x[j] = dropped(x[j], half_of(u, j), p.threshold, p.scale);
+      if (kResidual) x[j] += r[j];
+    }
+    store8t<kBf16>(p.out, at, x);
+  }
+}
+
+// Any row length: a warp takes 32 groups, forms their numbers, and passes
+// them through shared memory so that neighbouring lanes handle neighbouring
+// elements.
+template <bool kBf16, bool kResidual>
+__global__ void __launch_bounds__(256) dropout_ragged_kernel(const __grid_constant__ DropoutParams p) {
+  __shared__ uint4 numbers[8][32];
+  const RngKey key = rng_key(p.rng, p.site);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t step = gridDim.x * 256u;
+  for (uint32_t base = blockIdx.x * 256u + warp * 32u; base < p.total; base += step) {
+    const uint32_t i = base + lane;
+    long long at = 0;   // this lane's group: first element, and how many there are
+    int len = 0;
+    if (i < p.total) {
+      const int row = fdiv(static_cast<int>(i), p.fd_groups);
+      const int g = static_cast<int>(i) - row * p.groups;
+      at = static_cast<long long>(row) * p.cols + g * 8;
+      len = min(8, p.cols - g * 8);
+      numbers[warp][lane] = philox8(key, kRngDropout, static_cast<uint32_t>(row), static_cast<uint32_t>(g));
+    }
+    __syncwarp();
+    const uint16_t* u = reinterpret_cast<const uint16_t*>(numbers[warp]);
+#pragma unroll
+    for (int t = 0; t < 8; ++t) {
+      const int owner = t * 4 + (lane >> 3), j = lane & 7;
+      const long long e = __shfl_sync(0xffffffffu, at, owner) + j;
+      if (j < __shfl_sync(0xffffffffu, len, owner)) {
+        float x = dropped(load1t<kBf16>(p.x, e), u[owner * 8 + j], p.threshold, p.scale);
+        if (kResidual) x += load1t<kBf16>(p.residual, e);
+        store1t<kBf16>(p.out, e, x);
+      }
+    }
+    __syncwarp();
+  }
+}
+
+template <bool kBf16, bool kResidual>
+static cudaError_t launch_typed(const DropoutParams& p, int sms, cudaStream_t s) {
+  const uint32_t want = (p.total + 255) / 256, most = 32u * static_cast<uint32_t>(sms);
+  const uint32_t grid = want < most ? want : most;
+  if (p.cols % 8 == 0)
+    dropout_kernel<kBf16, kResidual><<<grid, 256, 0, s>>>(p);
+  else
+    dropout_ragged_kernel<kBf16, kResidual><<<grid, 256, 0, s>>>(p);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_dropout(const DropoutParams& p, bool bf16, int sms, cudaStream_t s) {
+  if (bf16) return p.residual ? launch_typed<true, true>(p, sms, s) : launch_typed<true, false>(p, sms, s);
+  return p.residual ? launch_typed<false, true>(p, sms, s) : launch_typed<false, false>(p, sms, s);
+}
+
+}  // namespace muon
