@@ -291,23 +291,45 @@ def readout_blend(theta, ema, out, w_final: float = 0.35, stream=None) -> None:
 
 
 # ------------------------------------------------------- dropout and 4 bits
-@dataclass
+# These calls are short (a few microseconds on the device), so their host side
+# is kept short too: no per-call imports, one pass over the tensors.
+_torch = None
+
+
+def _need_torch() -> None:
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+
+
 class Mxfp4:
-    """Matrices [count, rows, cols] in microscaled 4-bit floating point, blocks
+    """Matrices (count, rows, cols) in microscaled 4-bit floating point, blocks
     of 32 along cols. data: the codes, scales: one byte per block in tiles of
     128 rows x 4 blocks (both uint8; the header describes the layout)."""
-    data: "object"
-    scales: "object"
-    shape: Tuple[int, int, int]
+    __slots__ = ("data", "scales", "_shape", "_bytes")
+
+    def __init__(self, data, scales, shape):
+        _need_torch()
+        self.data, self.scales = data, scales
+        self._shape = _shape3(shape)
+        self._bytes = (int(_lib.muon_mxfp4_data_size(*self._shape)), int(_lib.muon_mxfp4_scales_size(*self._shape)))
+
+    @property
+    def shape(self) -> Tuple[int, int, int]:
+        return self._shape
+
+    def __repr__(self) -> str:
+        return f"Mxfp4(shape={self._shape}, device={self.data.device})"
 
 
 def _shape3(shape) -> Tuple[int, int, int]:
-    s = tuple(int(v) for v in shape)
+    s = tuple(shape)
     if len(s) == 2:
-        s = (1,) + s
+        return (1, int(s[0]), int(s[1]))
     if len(s) != 3:
         raise ValueError("expected (rows, cols) or (count, rows, cols)")
-    return s  # type: ignore[return-value]
+    return (int(s[0]), int(s[1]), int(s[2]))
 
 
 def alloc_mxfp4(shape, device="cuda") -> Mxfp4:
@@ -325,45 +347,41 @@ def alloc_mxfp4(shape, device="cuda") -> Mxfp4:
 def _cmx(q: Optional[Mxfp4], what: str):
     if q is None:
         return None
-    import torch
-    c, r, k = _shape3(q.shape)
-    n, m = _lib.muon_mxfp4_data_size(c, r, k), _lib.muon_mxfp4_scales_size(c, r, k)
-    if q.data.dtype != torch.uint8 or q.scales.dtype != torch.uint8:
+    n, m = q._bytes
+    d, s = q.data, q.scales
+    if d.dtype is not _torch.uint8 or s.dtype is not _torch.uint8:
         raise ValueError(f"{what}: data and scales must be uint8")
-    if n and (q.data.numel() != n or q.scales.numel() != m):
-        raise ValueError(f"{what}: storage of {q.data.numel()} + {q.scales.numel()} bytes for {n} + {m}")
-    return CMxfp4(c, r, k, _ptr(q.data), _ptr(q.scales))
+    if n and (d.numel() != n or s.numel() != m):
+        raise ValueError(f"{what}: storage of {d.numel()} + {s.numel()} bytes for {n} + {m}")
+    return CMxfp4(*q._shape, _ptr(d), _ptr(s))
 
 
-class _Launch:
-    """The device that a call's tensors share, made current for the call, and
-    the stream it runs on (the device's current one unless given)."""
-
-    def __init__(self, tensors, stream):
-        import torch
-        devices = {t.device for t in tensors if t is not None}
-        if len(devices) != 1 or next(iter(devices)).type != "cuda":
+def _launch(stream, fn, what, x, others, *args) -> None:
+    """fn(*args, stream) with the device of the call's tensors current, on the
+    given stream or that device's current one."""
+    _need_torch()
+    dev = x.get_device()
+    for t in others:
+        if t is not None and t.get_device() != dev:
             raise ValueError("the tensors of a call must be on one CUDA device")
-        self._guard = None
-        dev = next(iter(devices))
-        if dev.index != torch.cuda.current_device():
-            self._guard = torch.cuda.device(dev)
-        self._stream = stream
-
-    def __enter__(self):
-        if self._guard is not None:
-            self._guard.__enter__()
-        return _stream_handle(self._stream)
-
-    def __exit__(self, *exc):
-        if self._guard is not None:
-            self._guard.__exit__(*exc)
+    if dev < 0:
+        raise ValueError("the tensors of a call must be on one CUDA device")
+    if dev != _torch.cuda.current_device():
+        with _torch.cuda.device(dev):
+            code = fn(*args, _stream_handle(stream))
+    else:
+        code = fn(*args, _torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream_handle(stream))
+    if code != 0:
+        raise MuonError(code, what)
 
 
-def _check_rng(rng) -> None:
-    import torch
-    if rng is not None and (rng.dtype != torch.int64 or rng.numel() != 2):
+def _rng_ptr(rng):
+    if rng is None:
+        return None
+    _need_torch()
+    if rng.dtype is not _torch.int64 or rng.numel() != 2:
         raise ValueError("rng must be two int64: (seed, offset)")
+    return _ptr(rng)
 
 
 def dropout(x, out, p: float, rng, site: int = 0, residual=None, stream=None) -> None:
@@ -373,15 +391,16 @@ def dropout(x, out, p: float, rng, site: int = 0, residual=None, stream=None) ->
     device, site: the call's place within the step. The mask depends on them,
     the row and the column only; the gradient's pass is the same call on the
     output's gradient."""
-    _check_rng(rng)
-    for t, name in ((out, "out"), (residual, "residual")):
-        if t is not None and (t.shape != x.shape or t.dtype != x.dtype):
-            raise ValueError(f"{name} must have x's shape and dtype")
-    cols = x.shape[-1] if x.dim() else 1
+    shape = x.shape
+    if out.shape != shape or out.dtype != x.dtype:
+        raise ValueError("out must have x's shape and dtype")
+    if residual is not None and (residual.shape != shape or residual.dtype != x.dtype):
+        raise ValueError("residual must have x's shape and dtype")
+    r = _rng_ptr(rng)
+    cols = shape[-1] if len(shape) else 1
     rows = x.numel() // cols if cols else 0
-    with _Launch((x, out, rng, residual), stream) as s:
-        _check(_lib.muon_dropout(_ptr(x), _ptr(residual), _ptr(out), _dtype_code(x), rows, cols, p, _ptr(rng),
-                                 site, s), "dropout")
+    _launch(stream, _lib.muon_dropout, "dropout", x, (out, rng, residual), _ptr(x), _ptr(residual), _ptr(out),
+            _dtype_code(x), rows, cols, p, r, site)
 
 
 def mxfp4_quantize(x, out: Optional[Mxfp4] = None, out_t: Optional[Mxfp4] = None, dropout: float = 0.0,
@@ -392,13 +411,14 @@ def mxfp4_quantize(x, out: Optional[Mxfp4] = None, out_t: Optional[Mxfp4] = None
     same rng and site, x seen as [count * rows, cols]); stochastic rounds
     without bias, out and out_t independently. A block with an infinity or a
     NaN stands for NaN."""
-    _check_rng(rng)
     c, r, k = _shape3(x.shape)
-    q, qt = _cmx(out, "out"), _cmx(out_t, "out_t")
-    tensors = [x, rng] + [t for m in (out, out_t) if m is not None for t in (m.data, m.scales)]
-    with _Launch(tensors, stream) as s:
-        _check(_lib.muon_mxfp4_quantize(_ptr(x), _dtype_code(x), c, r, k, q, qt, dropout, 1 if stochastic else 0,
-                                        _ptr(rng), site, s), "mxfp4_quantize")
+    q, qt, g = _cmx(out, "out"), _cmx(out_t, "out_t"), _rng_ptr(rng)
+    _launch(stream, _lib.muon_mxfp4_quantize, "mxfp4_quantize", x, (rng, *_storage(out), *_storage(out_t)),
+            _ptr(x), _dtype_code(x), c, r, k, q, qt, dropout, 1 if stochastic else 0, g, site)
+
+
+def _storage(q: Optional[Mxfp4]):
+    return () if q is None else (q.data, q.scales)
 
 
 def mxfp4_readout(theta, ema, out: Optional[Mxfp4] = None, out_t: Optional[Mxfp4] = None,
@@ -409,20 +429,18 @@ def mxfp4_readout(theta, ema, out: Optional[Mxfp4] = None, out_t: Optional[Mxfp4
         raise ValueError("ema must be float32 of theta's shape")
     c, r, k = _shape3(theta.shape)
     q, qt = _cmx(out, "out"), _cmx(out_t, "out_t")
-    tensors = [theta, ema] + [t for m in (out, out_t) if m is not None for t in (m.data, m.scales)]
-    with _Launch(tensors, stream) as s:
-        _check(_lib.muon_mxfp4_readout(_ptr(theta), _dtype_code(theta), _ptr(ema), w_final, c, r, k, q, qt, s),
-               "mxfp4_readout")
+    _launch(stream, _lib.muon_mxfp4_readout, "mxfp4_readout", theta, (ema, *_storage(out), *_storage(out_t)),
+            _ptr(theta), _dtype_code(theta), _ptr(ema), w_final, c, r, k, q, qt)
 
 
 def mxfp4_dequantize(q: Mxfp4, out, stream=None) -> None:
     """out ([count, rows, cols] or [rows, cols], bf16 or fp32) = the values of
     q, exactly (2^128 and above become infinity)."""
     cq = _cmx(q, "q")
-    if _shape3(out.shape) != _shape3(q.shape):
+    if _shape3(out.shape) != q._shape:
         raise ValueError("out must have q's shape")
-    with _Launch((q.data, q.scales, out), stream) as s:
-        _check(_lib.muon_mxfp4_dequantize(cq, _ptr(out), _dtype_code(out), s), "mxfp4_dequantize")
+    _launch(stream, _lib.muon_mxfp4_dequantize, "mxfp4_dequantize", out, (q.data, q.scales), cq, _ptr(out),
+            _dtype_code(out))
 
 
 def matmul_workspace_size(a_shape, b_shape) -> int:
@@ -449,13 +467,15 @@ def mxfp4_matmul(a: Mxfp4, b: Mxfp4, out, workspace, add=None, stream=None) -> N
     be shared by calls that overlap on the device; device_status(workspace)
     reports a device-side wait that ran out."""
     ca, cb = _cmx(a, "a"), _cmx(b, "b")
-    if _shape3(out.shape) != (max(ca.count, cb.count), ca.rows, cb.rows):
+    (na, m, _), (nb, n, _) = a._shape, b._shape
+    shape = out.shape
+    if _shape3(shape) != (na if na > nb else nb, m, n):
         raise ValueError("out must be [count, a's rows, b's rows]")
-    if add is not None and (add.shape != out.shape or add.dtype != out.dtype):
+    if add is not None and (add.shape != shape or add.dtype != out.dtype):
         raise ValueError("add must have out's shape and dtype")
-    with _Launch((a.data, a.scales, b.data, b.scales, out, workspace, add), stream) as s:
-        _check(_lib.muon_mxfp4_matmul(ca, cb, _ptr(add), _ptr(out), _dtype_code(out), _ptr(workspace),
-                                      workspace.numel() * workspace.element_size(), s), "mxfp4_matmul")
+    _launch(stream, _lib.muon_mxfp4_matmul, "mxfp4_matmul", out,
+            (a.data, a.scales, b.data, b.scales, workspace, add), ca, cb, _ptr(add), _ptr(out), _dtype_code(out),
+            _ptr(workspace), workspace.numel() * workspace.element_size())
 
 
 def device_status(workspace, stream=None, clear: bool = False) -> int:

@@ -65,7 +65,7 @@ struct DequantParams {
 };
 
 cudaError_t launch_dropout(const DropoutParams& p, bool bf16, int sms, cudaStream_t s);
-cudaError_t launch_quantize(const QuantParams& p, bool bf16, cudaStream_t s);
+cudaError_t launch_quantize(const QuantParams& p, bool bf16, int sms, cudaStream_t s);
 cudaError_t launch_dequantize(const DequantParams& p, bool bf16, int sms, cudaStream_t s);
 
 // From api.cu: the current device's SM count, the tensor-map encoder (after

@@ -109,7 +109,7 @@ muon_status run_quantize(QuantParams& q, int32_t dtype, int64_t count, int64_t r
   q.tiles_c = static_cast<int>(ceil_div(cols, kMxTile));
   q.blocks_r = static_cast<int>(ceil_div(rows, kMxBlock));
   q.blocks_c = static_cast<int>(ceil_div(cols, kMxBlock));
-  return launch_quantize(q, dtype == MUON_BF16, static_cast<cudaStream_t>(stream)) == cudaSuccess
+  return launch_quantize(q, dtype == MUON_BF16, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess
              ? MUON_OK
              : MUON_ERR_CUDA;
 }
