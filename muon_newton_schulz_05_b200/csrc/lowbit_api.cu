@@ -300,6 +300,20 @@ muon_status muon_mxfp4_matmul(const muon_mxfp4* a, const muon_mxfp4* b, const vo
   const muon_mxfp4* r = pl.swap ? a : b;
   if ((st = operand_maps(l, 128, 1, &p.rows_l, &p.scales_l)) != MUON_OK) return st;
   if ((st = operand_maps(r, pl.few ? pl.nt : 128, pl.few ? 1 : 2, &p.rows_r, &p.scales_r)) != MUON_OK) return st;
+  // whole chunks are stored by TMA where out's rows start on 16-byte boundaries
+  p.tma_out = !pl.few && pl.split == 1 && !add && s.n * dtype_size(out_dtype) % 16 == 0 ? 1 : 0;
+  if (p.tma_out) {
+    const bool bf16 = out_dtype == MUON_BF16;
+    const cuuint64_t d[3] = {static_cast<cuuint64_t>(s.n), static_cast<cuuint64_t>(s.m),
+                             static_cast<cuuint64_t>(s.count)};
+    const cuuint64_t st2[2] = {static_cast<cuuint64_t>(s.n * dtype_size(out_dtype)),
+                               static_cast<cuuint64_t>(s.m * s.n * dtype_size(out_dtype))};
+    const cuuint32_t box[3] = {32, 32, 1};
+    if ((st = encode_tiled(&p.result, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3,
+                           out, d, st2, box, bf16 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B)) !=
+        MUON_OK)
+      return st;
+  }
   p.add = add;
   p.out = out;
   p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kHeader);

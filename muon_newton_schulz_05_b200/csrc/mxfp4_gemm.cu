@@ -3,15 +3,18 @@
 // in TMEM and one rounding at the end.
 //
 // Both kernels stage 256 elements of K at a time: 128-byte rows of codes
-// (TMA, 128-byte swizzle) and 512-byte scale tiles, which the MMA issuer
-// copies to TMEM (tcgen05.cp) right before the stage's four K = 64 MMAs.
+// (TMA, 128-byte swizzle) and 512-byte scale tiles, which go on to TMEM.
 //
 // pair kernel: clusters of 2 CTAs compute 256 x 256 tiles with the 2-SM MMA,
-// persistent over the tiles. Two 256-column accumulators and the scales do
-// not fit the 512 TMEM columns side by side, so the accumulators overlap by
-// 48 columns (0..255 and 208..463; scales above): the epilogue drains the
-// shared columns of a tile first, and the next tile's MMAs start as soon as
-// it has. Products with few tiles and a long K are split along K into fp32
+// persistent over the tiles. Four warps per CTA move the scales from shared
+// memory to TMEM (tcgen05.st), up to four stages ahead of the MMAs. (Copies
+// issued by the MMA thread, tcgen05.cp, take their turn in the tensor pipe:
+// the six of a stage cost it about 170 ns of 610, whether issued right before
+// the stage's MMAs or a stage ahead.)
+// Two 256-column accumulators and four scale buffers do not fit the 512 TMEM
+// columns side by side, so the accumulators overlap by 96 columns (0..255 and
+// 160..415; scales above): the epilogue drains the shared columns of a tile
+// first, and the next tile's MMAs start as soon as it has. Products with few tiles and a long K are split along K into fp32
 // partial tiles, which a second kernel adds in split order (deterministic).
 //
 // few-row kernel: for products with at most 128 rows on one side. The other
@@ -34,16 +37,23 @@ constexpr int kRows = 128;                         // operand rows per CTA and s
 constexpr int kCodeBytes = kRows * kKBytes;        // 16 KB
 constexpr int kSfGroupBytes = 2 * kMxTileBytes;    // scales of 128 rows and 256 K
 constexpr int kMxEpiWarps = 8;
-constexpr int kMxThreads = 64 + 32 * kMxEpiWarps;
+constexpr int kMxScaleWarps = 4;
+constexpr int kMxThreads = 64 + 32 * (kMxEpiWarps + kMxScaleWarps);
 
 // pair kernel
 constexpr int kPTile = 256;
-constexpr int kPStages = 6;
-constexpr int kPStageBytes = 2 * kCodeBytes + 3 * kSfGroupBytes;  // A, B half; A's 128 rows, B's 256
-constexpr int kPSmemBytes = kPStages * kPStageBytes + 1024 + 256;
-constexpr uint32_t kAccOffset = 208;               // first column of the second accumulator
-constexpr uint32_t kSfColumn = 464;                // two buffers of 24 columns
-constexpr uint32_t kSfBuf = 24;
+constexpr int kPStages = 5;
+constexpr int kPScaleBytes = 3 * kSfGroupBytes;    // A's 128 rows, B's 256
+constexpr int kPStageBytes = 2 * kCodeBytes + kPScaleBytes;
+constexpr int kPChunkBytes = 32 * 32 * 4;          // an epilogue warp's 32 x 32 chunk
+constexpr int kPSmemBytes = kPStages * kPStageBytes + kMxEpiWarps * kPChunkBytes + 1024 + 256;
+constexpr uint32_t kAccOffset = 160;               // first column of the second accumulator
+constexpr int kSfBufs = 4;
+constexpr uint32_t kSfBuf = 24;                    // A: 8 columns, B: 16
+constexpr uint32_t kSfColumn = 512 - kSfBufs * kSfBuf;
+constexpr int kOverlapChunks = 3;                  // 32-column chunks that the accumulators share
+static_assert(kAccOffset + kPTile <= kSfColumn, "the second accumulator ends below the scales");
+static_assert(kPTile - kAccOffset <= kOverlapChunks * 32, "the shared columns are drained first");
 
 __device__ __forceinline__ void drain(uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
   const uint32_t addr = smem_u32(bar);
@@ -77,33 +87,90 @@ __device__ __forceinline__ MxTile mx_tile(const MxGemmParams& p, int t) {
   return x;
 }
 
-// n consecutive outputs of one row, from column `col` on (cols exist up to p.n).
+// A warp's 32 x 32 chunk of fp32 results (one row per lane) as one TMA store,
+// through its shared-memory buffer (bf16: two half buffers in turn, 64-byte
+// swizzle; fp32: 128-byte swizzle; conflict-free either way).
 template <bool kBf16>
-__device__ __forceinline__ void store_row32(const MxGemmParams& p, long long base, int col, bool vec,
-                                            const uint32_t (&r)[32]) {
+__device__ __forceinline__ void store_chunk_tma(const MxGemmParams& p, uint8_t* buf, uint32_t turn, int lane,
+                                                const uint32_t* r, int c, int row, int col) {
+  if (kBf16) buf += (turn & 1u) * 2048;
+  if (lane == 0) bulk_wait_read<kBf16 ? 1 : 0>();   // the store that used this buffer has read it
+  __syncwarp();
+  if (kBf16) {
 #pragma unroll
-  for (int g = 0; g < 4; ++g) {
-    const int c = col + 8 * g;
-    if (vec && c + 8 <= p.n) {
-      float v[8];
+    for (int g = 0; g < 4; ++g) {
+      uint32_t w[4];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(r[8 * g + j]);
-      if (p.add) {
-        float a[8];
-        load8t<kBf16>(p.add, base + c, a);
+      for (int h = 0; h < 4; ++h)
+        w[h] = pack_bf16x2(__uint_as_float(r[8 * g + 2 * h]), __uint_as_float(r[8 * g + 2 * h + 1]));
+      *reinterpret_cast<uint4*>(buf + lane * 64 + ((g ^ ((lane >> 1) & 3)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] += a[j];
-      }
-      store8t<kBf16>(p.out, base + c, v);
-    } else {
+    for (int g = 0; g < 8; ++g)
+      *reinterpret_cast<uint4*>(buf + lane * 128 + ((g ^ (lane & 7)) << 4)) =
+          make_uint4(r[4 * g], r[4 * g + 1], r[4 * g + 2], r[4 * g + 3]);
+  }
+  fence_proxy_async_smem();
+  __syncwarp();
+  if (lane == 0 && row < p.m && col < p.n) tma_store_3d(&p.result, buf, col, row, c);
+  if (lane == 0) bulk_commit();
+}
+
+// The same for outputs that TMA cannot address, or with an addend: turned in
+// shared memory so that neighbouring lanes store neighbouring columns
+// (16-byte group g of row r lies at g ^ (r & 7)).
+template <bool kBf16>
+__device__ __forceinline__ void store_chunk(const MxGemmParams& p, uint8_t* buf, int lane, const uint32_t* r,
+                                            long long base, int row, int col, bool vec) {
+  __syncwarp();   // the previous chunk has been read
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        if (c + j < p.n) {
-          float v = __uint_as_float(r[8 * g + j]);
-          if (p.add) v += load1t<kBf16>(p.add, base + c + j);
-          store1t<kBf16>(p.out, base + c + j, v);
+  for (int g = 0; g < 8; ++g)
+    *reinterpret_cast<uint4*>(buf + lane * 128 + ((g ^ (lane & 7)) << 4)) =
+        make_uint4(r[4 * g], r[4 * g + 1], r[4 * g + 2], r[4 * g + 3]);
+  __syncwarp();
+  if (vec) {   // rows of a multiple of 4 elements: 8 lanes per row, 4 columns each
+    const int c = col + 4 * (lane & 7);
+    const int rows = c < p.n ? p.m - row : 0;
+    const long long at = base + static_cast<long long>(row + (lane >> 3)) * p.n + c;
+    float4 v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int rr = 4 * i + (lane >> 3);
+      v[i] = *reinterpret_cast<const float4*>(buf + rr * 128 + (((lane & 7) ^ (rr & 7)) << 4));
+    }
+    if (p.add) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (4 * i + (lane >> 3) < rows) {
+          if (kBf16) {
+            const uint2 a = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(p.add) + at + 4LL * i * p.n);
+            v[i].x += bf16_lo_f(a.x); v[i].y += bf16_hi_f(a.x); v[i].z += bf16_lo_f(a.y); v[i].w += bf16_hi_f(a.y);
+          } else {
+            const float4 a = *reinterpret_cast<const float4*>(static_cast<const float*>(p.add) + at + 4LL * i * p.n);
+            v[i].x += a.x; v[i].y += a.y; v[i].z += a.z; v[i].w += a.w;
+          }
         }
       }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (4 * i + (lane >> 3) < rows) {
+        if (kBf16)
+          *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + at + 4LL * i * p.n) =
+              make_uint2(pack_bf16x2(v[i].x, v[i].y), pack_bf16x2(v[i].z, v[i].w));
+        else
+          *reinterpret_cast<float4*>(static_cast<float*>(p.out) + at + 4LL * i * p.n) = v[i];
+      }
+    }
+  } else if (col + lane < p.n) {
+    const int rows = min(32, p.m - row);
+    const long long at = base + static_cast<long long>(row) * p.n + col + lane;
+#pragma unroll 8
+    for (int rr = 0; rr < rows; ++rr) {
+      float v = *reinterpret_cast<const float*>(buf + rr * 128 + (((lane >> 2) ^ (rr & 7)) << 4) + (lane & 3) * 4);
+      if (p.add) v += load1t<kBf16>(p.add, at + static_cast<long long>(rr) * p.n);
+      store1t<kBf16>(p.out, at + static_cast<long long>(rr) * p.n, v);
     }
   }
 }
@@ -116,9 +183,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
     mx_gemm_pair_kernel(const __grid_constant__ MxGemmParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kPStages * kPStageBytes);
-  uint64_t* empty = full + kPStages;
-  uint64_t* tfull = empty + kPStages;     // one per accumulator
+  uint8_t* chunks = smem + kPStages * kPStageBytes;
+  uint64_t* full = reinterpret_cast<uint64_t*>(chunks + kMxEpiWarps * kPChunkBytes);  // codes, both CTAs'
+  uint64_t* sfull = full + kPStages;      // scales, this CTA's
+  uint64_t* empty = sfull + kPStages;
+  uint64_t* sready = empty + kPStages;    // scales in TMEM, one per buffer
+  uint64_t* tfull = sready + kSfBufs;     // one per accumulator
   uint64_t* tnext = tfull + 2;            // the next tile's accumulator is free
   uint64_t* done = tnext + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
@@ -133,8 +203,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < kPStages; ++s) {
       mbar_init(&full[s], 1);
+      mbar_init(&sfull[s], 1);
       mbar_init(&empty[s], 1);
     }
+    for (int i = 0; i < kSfBufs; ++i) mbar_init(&sready[i], 2 * kMxScaleWarps);
     mbar_init(&tfull[0], 1);
     mbar_init(&tfull[1], 1);
     mbar_init(tnext, 2 * kMxEpiWarps);
@@ -179,26 +251,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
           }
           uint8_t* st = smem + stage * kPStageBytes;
           const uint32_t bar = full_leader + 8u * static_cast<uint32_t>(stage);
-          if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * kPStageBytes);
           const int k = T.kb0 + kb;
+          mbar_arrive_expect_tx(&sfull[stage], kPScaleBytes);
+          tma_load_2d(st + 2 * kCodeBytes, &p.scales_l, &sfull[stage], k * 256, ltile);
+          tma_load_2d(st + 2 * kCodeBytes + kSfGroupBytes, &p.scales_r, &sfull[stage], k * 256, rtile);
+          if (rank == 0) mbar_arrive_expect_tx(&full[stage], 4 * kCodeBytes);
           tma_load_3d_pair(st, &p.rows_l, bar, k * kKBytes, lrow, cl);
           tma_load_3d_pair(st + kCodeBytes, &p.rows_r, bar, k * kKBytes, rrow, cr);
-          tma_load_2d_pair(st + 2 * kCodeBytes, &p.scales_l, bar, k * 256, ltile);
-          tma_load_2d_pair(st + 2 * kCodeBytes + kSfGroupBytes, &p.scales_r, bar, k * 256, rtile);
           issued[stage] = static_cast<int>(phase);
           if (++stage == kPStages) { stage = 0; phase ^= 1u; }
         }
       }
-      if (rank == 0)
-        for (int s = 0; s < kPStages; ++s)
-          if (issued[s] >= 0) drain(&full[s], static_cast<uint32_t>(issued[s]), limit);
+      // every load has landed before shared memory is released
+      for (int s = 0; s < kPStages; ++s) {
+        if (issued[s] < 0) continue;
+        drain(&sfull[s], static_cast<uint32_t>(issued[s]), limit);
+        if (rank == 0) drain(&full[s], static_cast<uint32_t>(issued[s]), limit);
+      }
     }
   } else if (warp == 1) {
     if (lane == 0) {
       if (rank == 0) {
         // -------------------------------------------------- MMA issuer (leader)
-        int stage = 0, old_stage = kPStages - 2;   // old_stage: the one used two stages ago
-        uint32_t phase = 0, old_phase = 1, uses = 0;
+        int stage = 0;
+        uint32_t phase = 0, uses = 0;
         uint32_t acc = 0, tfree = 0;
         bool ok = true, first = true;
         for (int t = pair; ok && t < ntiles; t += npairs) {
@@ -211,25 +287,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
             tfree ^= 1u;
           }
           first = false;
-          tc_fence_after();
           const uint32_t d = tmem_base + acc * kAccOffset;
           for (int kb = 0; kb < T.nkb; ++kb) {
-            // the scale buffer is free once the MMAs of two stages ago are done
-            if ((uses >= 2 && !mbar_wait_cluster(&empty[old_stage], old_phase, abort_flag, p.status, limit)) ||
-                !mbar_wait_cluster(&full[stage], phase, abort_flag, p.status, limit)) {
+            const uint32_t buf = uses % kSfBufs;
+            if (!mbar_wait_cluster(&full[stage], phase, abort_flag, p.status, limit) ||
+                !mbar_wait_cluster(&sready[buf], (uses / kSfBufs) & 1u, abort_flag, p.status, limit)) {
               ok = false;
               break;
             }
             tc_fence_after();
-            const uint32_t a = smem_u32(smem + stage * kPStageBytes);
-            const uint32_t b = a + kCodeBytes, sa = b + kCodeBytes, sb = sa + kSfGroupBytes;
-            const uint32_t sfa = tmem_base + kSfColumn + (uses & 1u) * kSfBuf, sfb = sfa + 8;
-#pragma unroll
-            for (int g = 0; g < 2; ++g) {
-              tmem_copy_scales_pair(sfa + 4 * g, smem_desc_scales(sa + g * kMxTileBytes));
-              tmem_copy_scales_pair(sfb + 8 * g, smem_desc_scales(sb + g * kMxTileBytes));
-              tmem_copy_scales_pair(sfb + 8 * g + 4, smem_desc_scales(sb + kSfGroupBytes + g * kMxTileBytes));
-            }
+            const uint32_t a = smem_u32(smem + stage * kPStageBytes), b = a + kCodeBytes;
+            const uint32_t sfa = tmem_base + kSfColumn + buf * kSfBuf, sfb = sfa + 8;
             const int steps = min(4, p.k64 - 4 * (T.kb0 + kb));
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks) {
@@ -241,7 +309,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
             umma_commit_pair(&empty[stage]);
             ++uses;
             if (++stage == kPStages) { stage = 0; phase ^= 1u; }
-            if (++old_stage == kPStages) { old_stage = 0; old_phase ^= 1u; }
           }
           if (!ok) break;
           umma_commit_pair(&tfull[acc]);
@@ -251,6 +318,42 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
       }
       drain(done, 0, limit);
     }
+  } else if (warp >= 2 + kMxEpiWarps) {
+    // ------------------------------------------------------ scales to TMEM
+    // Word j of lane l of a scale tile belongs to row 32 j + l: that is TMEM
+    // column j, the same in all four lane quadrants (one per warp).
+    const uint32_t quad = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+    const uint32_t ready_leader = mapa_shared(smem_u32(sready), 0);
+    int stage = 0, old_stage = kPStages - kSfBufs;   // old_stage: the one used kSfBufs stages ago
+    uint32_t phase = 0, old_phase = 1, uses = 0;
+    bool ok = true;
+    for (int t = pair; ok && t < ntiles; t += npairs) {
+      const MxTile T = mx_tile(p, t);
+      for (int kb = 0; kb < T.nkb; ++kb) {
+        // a buffer is free once the MMAs that used it are done
+        const bool got = (uses < kSfBufs ||
+                          mbar_wait_cluster(&empty[old_stage], old_phase, abort_flag, p.status, limit)) &&
+                         mbar_wait(&sfull[stage], phase, abort_flag, p.status, limit);
+        if (!__all_sync(0xffffffffu, got)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint4* sf = reinterpret_cast<const uint4*>(smem + stage * kPStageBytes + 2 * kCodeBytes) + lane;
+        const uint32_t buf = uses % kSfBufs;
+        const uint32_t at = tmem_base + quad + kSfColumn + buf * kSfBuf;
+        // a 512-byte tile is 32 uint4; A: K halves 0, 1; B: row tile 0 halves 0, 1, row tile 1 halves 0, 1
+        tmem_st8(at, sf[0], sf[32]);
+        tmem_st16(at + 8, sf[64], sf[128], sf[96], sf[160]);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster_cta(ready_leader + 8u * buf);
+        ++uses;
+        if (++stage == kPStages) { stage = 0; phase ^= 1u; }
+        if (++old_stage == kPStages) { old_stage = 0; old_phase ^= 1u; }
+      }
+    }
   } else {
     // ------------------------------------------------------------ epilogue
     // warp w reads TMEM lanes 32 (w % 4) ..; warps 2..5 the accumulator's
@@ -258,7 +361,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
     // that the next tile's accumulator overlaps first.
     const int q = warp & 3, half = (warp - 2) >> 2;
     const uint32_t tnext_leader = mapa_shared(smem_u32(tnext), 0);
-    const bool vec = (p.n % 8) == 0;
+    const bool vec = (p.n % 4) == 0;
+    uint8_t* buf = chunks + (warp - 2) * kPChunkBytes;
     uint32_t acc = 0, phase = 0;
     bool ok = true;
     for (int t = pair; ok && t < ntiles; t += npairs) {
@@ -276,19 +380,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
       }
       tc_fence_after();
       const uint32_t tb = tmem_base + (static_cast<uint32_t>(32 * q) << 16) + acc * kAccOffset + half * 128;
-      const int row = T.im * kPTile + kRows * static_cast<int>(rank) + 32 * q + lane;
+      const int row = T.im * kPTile + kRows * static_cast<int>(rank) + 32 * q;
       const int col = T.in * kPTile + half * 128;
-#pragma unroll 1
-      for (int i = 0; i < 4; ++i) {
-        const int j = acc == 0 ? 3 - i : i;
-        uint32_t r[32];
-        tmem_ld32(tb + j * 32, r);
-        tmem_ld_wait();
-        if (overlapped && i == 1) {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_cluster_cta(tnext_leader);
-        }
+      auto store = [&](const uint32_t* r, int j) {
         if (kSplit) {
           // partial tile: the 32 x 32 chunk as 8 rows of 32 float4, one per lane
           float4* dst = reinterpret_cast<float4*>(
@@ -298,14 +392,36 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
           for (int g = 0; g < 8; ++g)
             dst[g * 32 + lane] = make_float4(__uint_as_float(r[4 * g]), __uint_as_float(r[4 * g + 1]),
                                              __uint_as_float(r[4 * g + 2]), __uint_as_float(r[4 * g + 3]));
-        } else if (row < p.m) {
-          const long long base = T.c * p.stride_c + static_cast<long long>(row) * p.n;
-          store_row32<kBf16>(p, base, col + j * 32, vec, r);
+        } else if (p.tma_out) {
+          store_chunk_tma<kBf16>(p, buf, static_cast<uint32_t>(j), lane, r, T.c, row, col + j * 32);
+        } else {
+          store_chunk<kBf16>(p, buf, lane, r, T.c * p.stride_c, row, col + j * 32, vec);
         }
+      };
+      uint32_t r[kOverlapChunks * 32];
+      // acc 0 shares its last chunks with the other accumulator, acc 1 its first
+      const int first = overlapped && acc == 0 ? 4 - kOverlapChunks : 0;
+#pragma unroll
+      for (int i = 0; i < kOverlapChunks; ++i)
+        tmem_ld32(tb + (first + i) * 32, *reinterpret_cast<uint32_t(*)[32]>(r + 32 * i));
+      tmem_ld_wait();
+      if (overlapped) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster_cta(tnext_leader);
       }
+#pragma unroll
+      for (int i = 0; i < kOverlapChunks; ++i) store(r + 32 * i, first + i);
+      const int rest = first == 0 ? kOverlapChunks : 0;
+      static_assert(kOverlapChunks == 3, "one chunk is left");
+      tmem_ld32(tb + rest * 32, *reinterpret_cast<uint32_t(*)[32]>(r));
+      tmem_ld_wait();
+      store(r, rest);
       acc ^= 1u;
       if (acc == 0) phase ^= 1u;
     }
+    if (lane == 0) bulk_wait_all();   // every bulk store of this warp has completed
+    __syncwarp();
   }
 
   tc_fence_before();

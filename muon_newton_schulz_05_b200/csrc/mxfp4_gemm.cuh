@@ -8,6 +8,8 @@ namespace muon {
 struct MxGemmParams {
   CUtensorMap rows_l, rows_r;      // codes: uint8 [count][rows][blocks * 16], 128-byte swizzle
   CUtensorMap scales_l, scales_r;  // scale tiles: uint32 [count * tiles][ceil(blocks / 4) * 128]
+  CUtensorMap result;              // pair kernel: out [count][m][n], boxes of 32 x 32 (if tma_out)
+  int tma_out;
   const void* add;
   void* out;
   float* part;                     // split products: fp32 partial tiles in the workspace
