@@ -434,44 +434,64 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
   }
 }
 
-// Adds the partial tiles of a split product in split order. One warp per
-// 32 x 32 chunk, turned through shared memory so that rows are stored whole.
+// Adds the partial tiles of a split product in split order. One block per
+// 32 x 32 chunk (a partial tile has 64): thread (g, lane) adds columns 4 g .. of
+// row `lane`, all parts on their way at once, and the chunk is turned in shared
+// memory so that rows are stored whole.
 template <bool kBf16>
 __global__ void __launch_bounds__(256) mx_reduce_kernel(const __grid_constant__ MxGemmParams p) {
-  __shared__ float turn[8][32][33];
+  __shared__ float turn[32][33];
   if (*reinterpret_cast<const volatile int*>(p.status) != 0) return;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int chunk = static_cast<int>(blockIdx.x & 7u) * 8 + warp;  // 64 chunks per tile, eight blocks
-  const int tile = static_cast<int>(blockIdx.x >> 3);
+  const int chunk = static_cast<int>(blockIdx.x & 63u), tile = static_cast<int>(blockIdx.x >> 6);
   const MxTile T = mx_tile(p, tile * p.split);
   const int j = chunk & 3, half = (chunk >> 2) & 1, q = (chunk >> 3) & 3, rank = chunk >> 5;
-  const int row0 = T.im * kPTile + kRows * rank + 32 * q, col = T.in * kPTile + half * 128 + j * 32 + lane;
-  float4 acc[8];
+  const int row0 = T.im * kPTile + kRows * rank + 32 * q, col0 = T.in * kPTile + half * 128 + j * 32;
+  if (row0 >= p.m || col0 >= p.n) return;
+  // this thread's output: four columns of row tid / 8
+  const int row = row0 + static_cast<int>(threadIdx.x >> 3), col = col0 + 4 * static_cast<int>(threadIdx.x & 7u);
+  const bool exists = row < p.m && col < p.n, vec = (p.n & 3) == 0;
+  const long long at = T.c * p.stride_c + static_cast<long long>(row) * p.n + col;
+  float add[4] = {0.f, 0.f, 0.f, 0.f};
+  if (p.add && exists) {
 #pragma unroll
-  for (int g = 0; g < 8; ++g) acc[g] = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int s = 0; s < p.split; ++s) {
-    const float4* src = reinterpret_cast<const float4*>(
-        p.part + (static_cast<long long>(tile) * p.split + s) * (kPTile * kPTile) + chunk * 1024);
+    for (int i = 0; i < 4; ++i)
+      if (col + i < p.n) add[i] = load1t<kBf16>(p.add, at + i);
+  }
+  const float4* src = reinterpret_cast<const float4*>(
+      p.part + static_cast<long long>(tile) * p.split * (kPTile * kPTile) + chunk * 1024) + threadIdx.x;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int s0 = 0; s0 < p.split; s0 += 8) {
+    float4 v[8];
 #pragma unroll
-    for (int g = 0; g < 8; ++g) {
-      const float4 v = src[g * 32 + lane];
-      acc[g].x += v.x; acc[g].y += v.y; acc[g].z += v.z; acc[g].w += v.w;
+    for (int s = 0; s < 8; ++s)
+      if (s0 + s < p.split) v[s] = src[static_cast<long long>(s0 + s) * (kPTile * kPTile / 4)];
+#pragma unroll
+    for (int s = 0; s < 8; ++s) {
+      if (s0 + s < p.split) {
+        acc.x += v[s].x; acc.y += v[s].y; acc.z += v[s].z; acc.w += v[s].w;
+      }
     }
   }
+  const int g = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  turn[lane][4 * g] = acc.x;
+  turn[lane][4 * g + 1] = acc.y;
+  turn[lane][4 * g + 2] = acc.z;
+  turn[lane][4 * g + 3] = acc.w;
+  __syncthreads();
+  if (!exists) return;
+  float y[4];
 #pragma unroll
-  for (int g = 0; g < 8; ++g) {
-    turn[warp][lane][4 * g] = acc[g].x;
-    turn[warp][lane][4 * g + 1] = acc[g].y;
-    turn[warp][lane][4 * g + 2] = acc[g].z;
-    turn[warp][lane][4 * g + 3] = acc[g].w;
-  }
-  __syncwarp();
-  if (col >= p.n) return;
-  for (int i = 0; i < 32 && row0 + i < p.m; ++i) {
-    const long long at = T.c * p.stride_c + static_cast<long long>(row0 + i) * p.n + col;
-    float v = turn[warp][i][lane];
-    if (p.add) v += load1t<kBf16>(p.add, at);
-    store1t<kBf16>(p.out, at, v);
+  for (int i = 0; i < 4; ++i) y[i] = turn[threadIdx.x >> 3][4 * (threadIdx.x & 7u) + i] + add[i];
+  if (vec) {
+    if (kBf16)
+      *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + at) =
+          make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
+    else
+      *reinterpret_cast<float4*>(static_cast<float*>(p.out) + at) = make_float4(y[0], y[1], y[2], y[3]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (col + i < p.n) store1t<kBf16>(p.out, at + i, y[i]);
   }
 }
 
@@ -480,6 +500,26 @@ __global__ void __launch_bounds__(256) mx_reduce_kernel(const __grid_constant__ 
 // takes K stages r * kc .. and the cluster adds the parts. 192 threads: warp 0
 // loads, warp 1 issues the MMAs, warps 2..5 are the epilogue.
 constexpr int kFewThreads = 192;
+constexpr int kFewSplit = 8;       // most CTAs per cluster
+
+// Four neighbouring outputs of one row (whose length is a multiple of 4).
+template <bool kBf16>
+__device__ __forceinline__ void store_quad(const MxGemmParams& p, long long at, float (&y)[4]) {
+  if (kBf16) {
+    if (p.add) {
+      const uint2 a = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(p.add) + at);
+      y[0] += bf16_lo_f(a.x); y[1] += bf16_hi_f(a.x); y[2] += bf16_lo_f(a.y); y[3] += bf16_hi_f(a.y);
+    }
+    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + at) =
+        make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
+  } else {
+    if (p.add) {
+      const float4 a = *reinterpret_cast<const float4*>(static_cast<const float*>(p.add) + at);
+      y[0] += a.x; y[1] += a.y; y[2] += a.z; y[3] += a.w;
+    }
+    *reinterpret_cast<float4*>(static_cast<float*>(p.out) + at) = make_float4(y[0], y[1], y[2], y[3]);
+  }
+}
 
 template <int NT>
 __host__ __device__ constexpr int few_stage_bytes() { return kCodeBytes + NT * kKBytes + 2 * kSfGroupBytes; }
@@ -506,6 +546,10 @@ __global__ void __launch_bounds__(kFewThreads) mx_gemm_few_kernel(const __grid_c
   const int kb0 = split * p.kc, nkb = min(p.kc, p.kstages - kb0);
 
   if (threadIdx.x == 0) {
+    tma_prefetch_map(&p.rows_l);
+    tma_prefetch_map(&p.rows_r);
+    tma_prefetch_map(&p.scales_l);
+    tma_prefetch_map(&p.scales_r);
     for (int s = 0; s < p.ring; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
@@ -627,21 +671,41 @@ __global__ void __launch_bounds__(kFewThreads) mx_gemm_few_kernel(const __grid_c
     if (threadIdx.x == 0) cluster_ok = ok ? 1 : 0;
     __syncthreads();
     cluster_sync();
-    bool all_ok = true;
-    for (int s = 0; s < p.split; ++s)
-      all_ok = all_ok && __float_as_int(ld_shared_cluster(mapa_shared(smem_u32(&cluster_ok), s))) != 0;
+    // CTA r of the cluster adds right rows r, r + split, ... : four left rows
+    // per thread, all parts loaded before the first is added
+    const uint32_t part0 = smem_u32(mine), ok0 = smem_u32(&cluster_ok);
+    uint32_t all_ok = 1;
+#pragma unroll
+    for (int s = 0; s < kFewSplit; ++s)
+      if (s < p.split) all_ok &= ld_shared_cluster_u32(mapa_shared(ok0, s));
     if (all_ok) {
-      const int per = (NT * kRows + p.split - 1) / p.split;
-      const int e1 = min((split + 1) * per, NT * kRows);
-      for (int e = split * per + static_cast<int>(threadIdx.x); e < e1; e += kFewThreads) {
-        const int x = e >> 7, l = im * kRows + (e & 127);
-        if (x >= p.n) break;
-        if (l >= p.m) continue;
-        float v = 0.0f;
-        for (int s = 0; s < p.split; ++s) v += ld_shared_cluster(mapa_shared(smem_u32(mine + e), s));
+      const int quads = (p.n - split + p.split - 1) / p.split * (kRows / 4);
+      for (int e = static_cast<int>(threadIdx.x); e < quads; e += kFewThreads) {
+        const int x = (e >> 5) * p.split + split, i = (e & 31) * 4;
+        float4 v[kFewSplit];
+#pragma unroll
+        for (int s = 0; s < kFewSplit; ++s)
+          if (s < p.split) v[s] = ld_shared_cluster_f32x4(mapa_shared(part0 + (x * kRows + i) * 4, s));
+        float y[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
+#pragma unroll
+        for (int s = 1; s < kFewSplit; ++s) {
+          if (s < p.split) {
+            y[0] += v[s].x; y[1] += v[s].y; y[2] += v[s].z; y[3] += v[s].w;
+          }
+        }
+        const int l = im * kRows + i;
         const long long at = c * p.stride_c + l * p.stride_l + x * p.stride_r;
-        if (p.add) v += load1t<kBf16>(p.add, at);
-        store1t<kBf16>(p.out, at, v);
+        if (p.stride_l == 1 && (p.stride_r & 3) == 0) {   // four neighbours of one row of out
+          if (l < p.m) store_quad<kBf16>(p, at, y);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            if (l + j < p.m) {
+              if (p.add) y[j] += load1t<kBf16>(p.add, at + j * p.stride_l);
+              store1t<kBf16>(p.out, at + j * p.stride_l, y[j]);
+            }
+          }
+        }
       }
     }
     cluster_sync();   // the others have read this CTA's part
@@ -665,10 +729,10 @@ MxGemmPlan plan_mx_gemm(const MxGemmShape& s, int pairs, int sms) {
     pl.nt = small <= 16 ? 16 : small <= 32 ? 32 : small <= 64 ? 64 : 128;
     pl.tm = static_cast<int>((large + kRows - 1) / kRows);
     pl.tn = 1;
-    // split K over the CTAs of a cluster (a power of two, up to 8) while that
+    // split K over the CTAs of a cluster (a power of two) while that
     // still adds CTAs the device has room for
     pl.split = 1;
-    while (pl.split < 8 && pl.split * 2 <= kstages && s.count * pl.tm * pl.split * 2 <= 2 * sms) pl.split *= 2;
+    while (pl.split < kFewSplit && pl.split * 2 <= kstages && s.count * pl.tm * pl.split * 2 <= 2 * sms) pl.split *= 2;
     pl.kc = (kstages + pl.split - 1) / pl.split;
     while (pl.split > 1 && pl.kc * (pl.split - 1) >= kstages) {  // no empty part
       pl.split /= 2;
@@ -761,7 +825,7 @@ cudaError_t launch_mx_gemm(const MxGemmParams& p, const MxGemmPlan& plan, bool b
   cfg.dynamicSmemBytes = kPSmemBytes;
   cudaError_t e = cudaLaunchKernelExC(&cfg, pair_kernel(bf16, plan.split > 1), args);
   if (e != cudaSuccess || plan.split == 1) return e;
-  const unsigned blocks = static_cast<unsigned>(tiles) * 8u;
+  const unsigned blocks = static_cast<unsigned>(tiles) * 64u;
   if (bf16)
     mx_reduce_kernel<true><<<blocks, 256, 0, s>>>(p);
   else
