@@ -38,15 +38,17 @@ constexpr int kCodeBytes = kRows * kKBytes;        // 16 KB
 constexpr int kSfGroupBytes = 2 * kMxTileBytes;    // scales of 128 rows and 256 K
 constexpr int kMxEpiWarps = 8;
 constexpr int kMxScaleWarps = 4;
-constexpr int kMxThreads = 64 + 32 * (kMxEpiWarps + kMxScaleWarps);
+constexpr int kMxThreads = 96 + 32 * (kMxEpiWarps + kMxScaleWarps);
 
 // pair kernel
 constexpr int kPTile = 256;
 constexpr int kPStages = 5;
+constexpr int kPStageBytes = 2 * kCodeBytes;
+constexpr int kSfSlots = 8;                        // the scales' own ring
 constexpr int kPScaleBytes = 3 * kSfGroupBytes;    // A's 128 rows, B's 256
-constexpr int kPStageBytes = 2 * kCodeBytes + kPScaleBytes;
 constexpr int kPChunkBytes = 32 * 32 * 4;          // an epilogue warp's 32 x 32 chunk
-constexpr int kPSmemBytes = kPStages * kPStageBytes + kMxEpiWarps * kPChunkBytes + 1024 + 256;
+constexpr int kPSmemBytes =
+    kPStages * kPStageBytes + kSfSlots * kPScaleBytes + kMxEpiWarps * kPChunkBytes + 1024 + 512;
 constexpr uint32_t kAccOffset = 160;               // first column of the second accumulator
 constexpr int kSfBufs = 4;
 constexpr uint32_t kSfBuf = 24;                    // A: 8 columns, B: 16
@@ -183,11 +185,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
     mx_gemm_pair_kernel(const __grid_constant__ MxGemmParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* chunks = smem + kPStages * kPStageBytes;
+  uint8_t* slots = smem + kPStages * kPStageBytes;
+  uint8_t* chunks = slots + kSfSlots * kPScaleBytes;
   uint64_t* full = reinterpret_cast<uint64_t*>(chunks + kMxEpiWarps * kPChunkBytes);  // codes, both CTAs'
-  uint64_t* sfull = full + kPStages;      // scales, this CTA's
-  uint64_t* empty = sfull + kPStages;
-  uint64_t* sready = empty + kPStages;    // scales in TMEM, one per buffer
+  uint64_t* empty = full + kPStages;
+  uint64_t* sfull = empty + kPStages;     // scales in shared memory, this CTA's
+  uint64_t* sempty = sfull + kSfSlots;
+  uint64_t* sready = sempty + kSfSlots;   // scales in TMEM, one per buffer
   uint64_t* tfull = sready + kSfBufs;     // one per accumulator
   uint64_t* tnext = tfull + 2;            // the next tile's accumulator is free
   uint64_t* done = tnext + 1;
@@ -203,8 +207,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < kPStages; ++s) {
       mbar_init(&full[s], 1);
-      mbar_init(&sfull[s], 1);
       mbar_init(&empty[s], 1);
+    }
+    for (int s = 0; s < kSfSlots; ++s) {
+      mbar_init(&sfull[s], 1);
+      mbar_init(&sempty[s], kMxScaleWarps);
     }
     for (int i = 0; i < kSfBufs; ++i) mbar_init(&sready[i], 2 * kMxScaleWarps);
     mbar_init(&tfull[0], 1);
@@ -242,8 +249,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
         const int cl = p.share_l ? 0 : T.c, cr = p.share_r ? 0 : T.c;
         const int lrow = T.im * kPTile + kRows * static_cast<int>(rank);
         const int rrow = T.in * kPTile + kRows * static_cast<int>(rank);
-        const int ltile = cl * p.tiles_l + 2 * T.im + static_cast<int>(rank);
-        const int rtile = cr * p.tiles_r + 2 * T.in;
         for (int kb = 0; kb < T.nkb; ++kb) {
           if (!mbar_wait_cluster(&empty[stage], phase ^ 1u, abort_flag, p.status, limit)) {
             ok = false;
@@ -252,9 +257,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
           uint8_t* st = smem + stage * kPStageBytes;
           const uint32_t bar = full_leader + 8u * static_cast<uint32_t>(stage);
           const int k = T.kb0 + kb;
-          mbar_arrive_expect_tx(&sfull[stage], kPScaleBytes);
-          tma_load_2d(st + 2 * kCodeBytes, &p.scales_l, &sfull[stage], k * 256, ltile);
-          tma_load_2d(st + 2 * kCodeBytes + kSfGroupBytes, &p.scales_r, &sfull[stage], k * 256, rtile);
           if (rank == 0) mbar_arrive_expect_tx(&full[stage], 4 * kCodeBytes);
           tma_load_3d_pair(st, &p.rows_l, bar, k * kKBytes, lrow, cl);
           tma_load_3d_pair(st + kCodeBytes, &p.rows_r, bar, k * kKBytes, rrow, cr);
@@ -263,20 +265,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
         }
       }
       // every load has landed before shared memory is released
-      for (int s = 0; s < kPStages; ++s) {
-        if (issued[s] < 0) continue;
-        drain(&sfull[s], static_cast<uint32_t>(issued[s]), limit);
-        if (rank == 0) drain(&full[s], static_cast<uint32_t>(issued[s]), limit);
-      }
+      if (rank == 0)
+        for (int s = 0; s < kPStages; ++s)
+          if (issued[s] >= 0) drain(&full[s], static_cast<uint32_t>(issued[s]), limit);
     }
   } else if (warp == 1) {
     if (lane == 0) {
       if (rank == 0) {
         // -------------------------------------------------- MMA issuer (leader)
+        // The tensor pipe holds few MMAs, so the time between the last one of a
+        // stage and the first one of the next must be short: the next stage's
+        // barriers are looked at in the middle of this one, and descriptors
+        // differ by additions only (K step: 32 bytes, stage: kPStageBytes).
+        const uint64_t desc0 = smem_desc_sw128(smem_u32(smem), 16, 1024);
         int stage = 0;
         uint32_t phase = 0, uses = 0;
         uint32_t acc = 0, tfree = 0;
-        bool ok = true, first = true;
+        bool ok = true, first = true, ready = false;
         for (int t = pair; ok && t < ntiles; t += npairs) {
           const MxTile T = mx_tile(p, t);
           if (!first) {
@@ -290,25 +295,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
           const uint32_t d = tmem_base + acc * kAccOffset;
           for (int kb = 0; kb < T.nkb; ++kb) {
             const uint32_t buf = uses % kSfBufs;
-            if (!mbar_wait_cluster(&full[stage], phase, abort_flag, p.status, limit) ||
-                !mbar_wait_cluster(&sready[buf], (uses / kSfBufs) & 1u, abort_flag, p.status, limit)) {
+            if (!ready &&
+                (!mbar_wait_cluster(&full[stage], phase, abort_flag, p.status, limit) ||
+                 !mbar_wait_cluster(&sready[buf], (uses / kSfBufs) & 1u, abort_flag, p.status, limit))) {
               ok = false;
               break;
             }
             tc_fence_after();
-            const uint32_t a = smem_u32(smem + stage * kPStageBytes), b = a + kCodeBytes;
+            const uint64_t a = desc0 + static_cast<uint32_t>(stage * (kPStageBytes >> 4)), b = a + (kCodeBytes >> 4);
             const uint32_t sfa = tmem_base + kSfColumn + buf * kSfBuf, sfb = sfa + 8;
             const int steps = min(4, p.k64 - 4 * (T.kb0 + kb));
+            const uint64_t* used = &empty[stage];
+            ++uses;
+            if (++stage == kPStages) { stage = 0; phase ^= 1u; }
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks) {
               if (ks < steps)
-                umma_mxf4_pair(d, smem_desc_sw128(a + ks * 32, 16, 1024), smem_desc_sw128(b + ks * 32, 16, 1024),
-                               idesc_mxf4(kPTile, kPTile, 2 * (ks & 1)), sfa + 4 * (ks >> 1), sfb + 8 * (ks >> 1),
-                               (kb > 0 || ks > 0) ? 1u : 0u);
+                umma_mxf4_pair(d, a + 2 * ks, b + 2 * ks, idesc_mxf4(kPTile, kPTile, 2 * (ks & 1)),
+                               sfa + 4 * (ks >> 1), sfb + 8 * (ks >> 1), (kb > 0 || ks > 0) ? 1u : 0u);
+              if (ks == 1)
+                ready = mbar_try_wait_cluster(smem_u32(&full[stage]), phase) &&
+                        mbar_try_wait_cluster(smem_u32(&sready[uses % kSfBufs]), (uses / kSfBufs) & 1u);
             }
-            umma_commit_pair(&empty[stage]);
-            ++uses;
-            if (++stage == kPStages) { stage = 0; phase ^= 1u; }
+            umma_commit_pair(const_cast<uint64_t*>(used));
           }
           if (!ok) break;
           umma_commit_pair(&tfull[acc]);
@@ -318,39 +327,74 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
       }
       drain(done, 0, limit);
     }
+  } else if (warp == 2 + kMxEpiWarps + kMxScaleWarps) {
+    if (lane == 0) {
+      // ---------------------------------------------------- scale producer
+      int slot = 0;
+      uint32_t phase = 0;
+      int issued[kSfSlots];
+      for (int s = 0; s < kSfSlots; ++s) issued[s] = -1;
+      bool ok = true;
+      for (int t = pair; ok && t < ntiles; t += npairs) {
+        const MxTile T = mx_tile(p, t);
+        const int ltile = (p.share_l ? 0 : T.c) * p.tiles_l + 2 * T.im + static_cast<int>(rank);
+        const int rtile = (p.share_r ? 0 : T.c) * p.tiles_r + 2 * T.in;
+        for (int kb = 0; kb < T.nkb; ++kb) {
+          if (!mbar_wait(&sempty[slot], phase ^ 1u, abort_flag, p.status, limit)) {
+            ok = false;
+            break;
+          }
+          uint8_t* at = slots + slot * kPScaleBytes;
+          mbar_arrive_expect_tx(&sfull[slot], kPScaleBytes);
+          tma_load_2d(at, &p.scales_l, &sfull[slot], (T.kb0 + kb) * 256, ltile);
+          tma_load_2d(at + kSfGroupBytes, &p.scales_r, &sfull[slot], (T.kb0 + kb) * 256, rtile);
+          issued[slot] = static_cast<int>(phase);
+          if (++slot == kSfSlots) { slot = 0; phase ^= 1u; }
+        }
+      }
+      for (int s = 0; s < kSfSlots; ++s)
+        if (issued[s] >= 0) drain(&sfull[s], static_cast<uint32_t>(issued[s]), limit);
+    }
   } else if (warp >= 2 + kMxEpiWarps) {
     // ------------------------------------------------------ scales to TMEM
     // Word j of lane l of a scale tile belongs to row 32 j + l: that is TMEM
     // column j, the same in all four lane quadrants (one per warp).
     const uint32_t quad = static_cast<uint32_t>(32 * (warp & 3)) << 16;
     const uint32_t ready_leader = mapa_shared(smem_u32(sready), 0);
-    int stage = 0, old_stage = kPStages - kSfBufs;   // old_stage: the one used kSfBufs stages ago
+    int old_stage = kPStages - kSfBufs, slot = 0;   // old_stage: the one used kSfBufs stages ago
     uint32_t phase = 0, old_phase = 1, uses = 0;
     bool ok = true;
     for (int t = pair; ok && t < ntiles; t += npairs) {
       const MxTile T = mx_tile(p, t);
       for (int kb = 0; kb < T.nkb; ++kb) {
+        // the scales have landed; take them to registers and free the slot
+        if (!__all_sync(0xffffffffu, mbar_wait(&sfull[slot], phase, abort_flag, p.status, limit))) {
+          ok = false;
+          break;
+        }
+        const uint4* sf = reinterpret_cast<const uint4*>(slots + slot * kPScaleBytes) + lane;
+        // a 512-byte tile is 32 uint4; A: K halves 0, 1; B: row tile 0 halves 0, 1, row tile 1 halves 0, 1
+        const uint4 a0 = sf[0], a1 = sf[32], b00 = sf[64], b01 = sf[96], b10 = sf[128], b11 = sf[160];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sempty[slot]);
         // a buffer is free once the MMAs that used it are done
-        const bool got = (uses < kSfBufs ||
-                          mbar_wait_cluster(&empty[old_stage], old_phase, abort_flag, p.status, limit)) &&
-                         mbar_wait(&sfull[stage], phase, abort_flag, p.status, limit);
-        if (!__all_sync(0xffffffffu, got)) {
+        if (uses >= kSfBufs &&
+            !__all_sync(0xffffffffu,
+                        mbar_wait_cluster(&empty[old_stage], old_phase, abort_flag, p.status, limit))) {
           ok = false;
           break;
         }
         tc_fence_after();
-        const uint4* sf = reinterpret_cast<const uint4*>(smem + stage * kPStageBytes + 2 * kCodeBytes) + lane;
         const uint32_t buf = uses % kSfBufs;
         const uint32_t at = tmem_base + quad + kSfColumn + buf * kSfBuf;
-        // a 512-byte tile is 32 uint4; A: K halves 0, 1; B: row tile 0 halves 0, 1, row tile 1 halves 0, 1
-        tmem_st8(at, sf[0], sf[32]);
-        tmem_st16(at + 8, sf[64], sf[128], sf[96], sf[160]);
+        tmem_st8(at, a0, a1);
+        tmem_st16(at + 8, b00, b10, b01, b11);
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive_cluster_cta(ready_leader + 8u * buf);
         ++uses;
-        if (++stage == kPStages) { stage = 0; phase ^= 1u; }
+        if (++slot == kSfSlots) { slot = 0; phase ^= 1u; }
         if (++old_stage == kPStages) { old_stage = 0; old_phase ^= 1u; }
       }
     }
