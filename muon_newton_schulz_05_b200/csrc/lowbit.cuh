@@ -57,7 +57,7 @@ struct QuantParams {
 struct DequantParams {
   const uint8_t *q, *s;
   void* out;
-  int rows, cols;
+  int count, rows, cols;
   int blocks, tiles_r, tiles_c;
   int groups;                   // ceil(cols / 8)
   FastDiv fd_groups, fd_rows;

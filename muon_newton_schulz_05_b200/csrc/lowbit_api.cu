@@ -251,6 +251,7 @@ muon_status muon_mxfp4_dequantize(const muon_mxfp4* q, void* out, int32_t dtype,
   d.q = static_cast<const uint8_t*>(q->data);
   d.s = static_cast<const uint8_t*>(q->scales);
   d.out = out;
+  d.count = static_cast<int>(q->count);
   d.rows = static_cast<int>(q->rows);
   d.cols = static_cast<int>(q->cols);
   d.blocks = static_cast<int>(ceil_div(q->cols, kMxBlock));

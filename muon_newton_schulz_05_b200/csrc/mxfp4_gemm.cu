@@ -283,7 +283,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
         uint32_t acc = 0, tfree = 0;
         bool ok = true, first = true, ready = false;
         for (int t = pair; ok && t < ntiles; t += npairs) {
-          const MxTile T = mx_tile(p, t);
+          const int kb0 = p.split == 1 ? 0 : t % p.split * p.kc;
+          const int nkb = min(p.kc, p.kstages - kb0);
           if (!first) {
             if (!mbar_wait_cluster(tnext, tfree, abort_flag, p.status, limit)) {
               ok = false;
@@ -293,7 +294,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
           }
           first = false;
           const uint32_t d = tmem_base + acc * kAccOffset;
-          for (int kb = 0; kb < T.nkb; ++kb) {
+          for (int kb = 0; kb < nkb; ++kb) {
             const uint32_t buf = uses % kSfBufs;
             if (!ready &&
                 (!mbar_wait_cluster(&full[stage], phase, abort_flag, p.status, limit) ||
@@ -304,7 +305,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
             tc_fence_after();
             const uint64_t a = desc0 + static_cast<uint32_t>(stage * (kPStageBytes >> 4)), b = a + (kCodeBytes >> 4);
             const uint32_t sfa = tmem_base + kSfColumn + buf * kSfBuf, sfb = sfa + 8;
-            const int steps = min(4, p.k64 - 4 * (T.kb0 + kb));
+            const int steps = min(4, p.k64 - 4 * (kb0 + kb));
             const uint64_t* used = &empty[stage];
             ++uses;
             if (++stage == kPStages) { stage = 0; phase ^= 1u; }
@@ -314,8 +315,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
                 umma_mxf4_pair(d, a + 2 * ks, b + 2 * ks, idesc_mxf4(kPTile, kPTile, 2 * (ks & 1)),
                                sfa + 4 * (ks >> 1), sfb + 8 * (ks >> 1), (kb > 0 || ks > 0) ? 1u : 0u);
               if (ks == 1)
-                ready = mbar_try_wait_cluster(smem_u32(&full[stage]), phase) &&
-                        mbar_try_wait_cluster(smem_u32(&sready[uses % kSfBufs]), (uses / kSfBufs) & 1u);
+                ready = mbar_test_cluster(&full[stage], phase) &&
+                        mbar_test_cluster(&sready[uses % kSfBufs], (uses / kSfBufs) & 1u);
             }
             umma_commit_pair(const_cast<uint64_t*>(used));
           }

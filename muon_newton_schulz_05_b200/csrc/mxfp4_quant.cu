@@ -41,49 +41,62 @@ __device__ __forceinline__ uint32_t block_scale(float amax, float& inv) {
   return byte;
 }
 
-// Codes of two values already in e2m1's range: lo in bits 0..3, hi in 4..7.
-__device__ __forceinline__ uint32_t pack_e2m1(float lo, float hi) {
-  uint16_t r;
-  asm("{\n\t.reg .b8 t;\n\tcvt.rn.satfinite.e2m1x2.f32 t, %1, %2;\n\tmov.b16 %0, {t, 0};\n\t}"
-      : "=h"(r)
-      : "f"(hi), "f"(lo));
-  return r;
+// The codes of eight values already in e2m1's range, the first in the low bits.
+__device__ __forceinline__ uint32_t pack8_e2m1(const float (&y)[8]) {
+  uint32_t w;
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+      "mov.b32 %0, {a, b, c, d};\n\t}"
+      : "=r"(w)
+      : "f"(y[0]), "f"(y[1]), "f"(y[2]), "f"(y[3]), "f"(y[4]), "f"(y[5]), "f"(y[6]), "f"(y[7]));
+  return w;
 }
 
-// Stochastic code of y (|y| <= 6): between the neighbours of |y|, up when the
-// 16-bit number plus one half is below the fraction times 2^16 (all exact).
-__device__ __forceinline__ uint32_t stochastic_e2m1(float y, uint32_t u16) {
-  const float a = fabsf(y);
-  const float steps = a < 2.0f ? 2.0f * a : (a < 4.0f ? a : 0.5f * a);
-  const uint32_t base = a < 2.0f ? 0u : (a < 4.0f ? 2u : 4u);
-  const float low = floorf(steps);
-  const bool up = static_cast<float>(u16) + 0.5f < (steps - low) * 65536.0f;
-  return (static_cast<uint32_t>(low) + base + (up ? 1u : 0u)) | (__float_as_uint(y) >> 31 << 3);
-}
-
-// The eight codes of eight values of one block, in a 32-bit word. (mul, the
-// dropout factor, and inv are applied one after the other: the first product
-// is rounded, the second one is exact.)
-template <bool kMul>
-__device__ __forceinline__ uint32_t code8(const float (&v)[8], float mul, float inv) {
-  uint32_t b[4];
-#pragma unroll
-  for (int j = 0; j < 4; ++j)
-    b[j] = kMul ? pack_e2m1(v[2 * j] * mul * inv, v[2 * j + 1] * mul * inv)
-                : pack_e2m1(v[2 * j] * inv, v[2 * j + 1] * inv);
-  return __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
-}
-
-__device__ __forceinline__ uint32_t code8_stochastic(const float (&v)[8], float mul, float inv, const uint4& u) {
+// Stochastic codes of eight values with |y| <= 6: between the neighbours of
+// |y|, up when the 16-bit number u plus one half is below the fraction times
+// 2^16. With E = max(0, exponent of y), the gap is 2^(E - 1), the code of the
+// lower neighbour floor(|y| 2^(1 - E)) + 2 E, and the one wanted
+// ceil((|y| 2^(17 - E) - (u + 1/2)) 2^-16) + 2 E. The difference has the exact
+// sign, and is exact where it is near a multiple of 2^16 (a multiple of 2^-7
+// below 2^18), so the ceiling, taken by adding 1.5 * 2^23 with rounding
+// upwards, is that of the exact value.
+__device__ __forceinline__ uint32_t pack8_stochastic(const float (&y)[8], const uint4& u) {
   const uint32_t uu[4] = {u.x, u.y, u.z, u.w};
   uint32_t w = 0;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    w |= stochastic_e2m1(v[2 * j] * mul * inv, uu[j] & 0xFFFFu) << (8 * j);
-    w |= stochastic_e2m1(v[2 * j + 1] * mul * inv, uu[j] >> 16) << (8 * j + 4);
+  for (int j = 0; j < 8; ++j) {
+    const uint32_t u16 = (j & 1) ? uu[j >> 1] >> 16 : uu[j >> 1] & 0xFFFFu;
+    const float half_up = __uint_as_float(0x4B000000u | u16) - 8388607.5f;        // u16 + 1/2
+    const uint32_t e = __float_as_uint(fmaxf(fabsf(y[j]), 1.0f)) & 0x7F800000u;
+    const float k = __uint_as_float(0x48000000u + 0x3F800000u - e);               // 2^(17 - E)
+    const float d = fmaf(fabsf(y[j]), k, -half_up);
+    const uint32_t c = __float_as_uint(__fmaf_ru(d, 1.0f / 65536.0f, 12582912.0f));
+    // 1.5 * 2^23 has the bits 0x4B400000, E is (e >> 23) - 127
+    const uint32_t code = c + (e >> 22) - (0x4B400000u + 254u) + ((__float_as_uint(y[j]) >> 28) & 8u);
+    w |= code << (4 * j);
   }
   return w;
 }
+
+__device__ __forceinline__ uint32_t max_abs_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("{\n\t.reg .b32 x, y;\n\tabs.bf16x2 x, %1;\n\tabs.bf16x2 y, %2;\n\tmax.NaN.bf16x2 %0, x, y;\n\t}"
+      : "=r"(r)
+      : "r"(a), "r"(b));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// A power of two (or 0) as bf16, its upper half word.
+__device__ __forceinline__ uint32_t bf16_bits(float pow2) { return __float_as_uint(pow2) >> 16; }
 
 enum QuantSrc : int { kSrcBf16 = 0, kSrcF32 = 1, kSrcBlendBf16 = 2, kSrcBlendF32 = 3 };
 
@@ -132,141 +145,216 @@ __device__ __forceinline__ QuantTile quant_tile(const QuantParams& p, int t) {
   return x;
 }
 
-// Copies a tile to shared memory, 16 bytes at a time: asynchronously where
-// rows start on 16-byte boundaries, else through registers; what lies outside
-// the matrix becomes zero. The blend is formed here, with the roundings of
-// readout_blend.
+__device__ __forceinline__ void copy4_async(void* dst, const void* src, bool exists) {
+  const int n = exists ? 4 : 0;
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(n) : "memory");
+}
+
+// Byte offset of element `col` in a tile row.
+template <bool kHalf>
+__device__ __forceinline__ int tile_offset(int lr, int col) {
+  constexpr int kPer = kHalf ? 8 : 4, kElt = kHalf ? 2 : 4;
+  return 16 * swizzled_group(lr, col / kPer) + (col % kPer) * kElt;
+}
+
+// Copies a tile to shared memory; what lies outside the matrix becomes zero.
+// Asynchronously in 16-byte pieces where rows start on 16-byte boundaries, in
+// 4-byte pieces where they start on 4-byte boundaries, else (bf16, odd length)
+// through registers. The blend is formed here, with readout_blend's roundings.
 template <int kSrc>
 __device__ __forceinline__ void fill_tile(const QuantParams& p, uint8_t* tile, const QuantTile& T) {
   using C = QuantConfig<kSrc>;
-  constexpr int kPer = C::kHalf ? 8 : 4;                        // elements per 16-byte group
-  constexpr int kGroups = kMxTile / kPer;                       // groups per row
-  constexpr int kEach = kMxTile * kGroups / C::kThreads;
   constexpr int kElt = C::kBf16 ? 2 : 4;
-  const bool vec = p.cols % 8 == 0;
-  const int g = threadIdx.x % kGroups;
-  const int col = T.c0 + g * kPer;
-  const int n = p.cols - col;
-  if (!C::kBlend && vec) {
+  const int tid = threadIdx.x;
+  const long long first = (static_cast<long long>(T.mat) * p.rows + T.r0) * p.cols + T.c0;
+  const int rows = p.rows - T.r0, cols = p.cols - T.c0;   // from the tile's corner on
+  if constexpr (!C::kBlend) {
+    const uint8_t* src = static_cast<const uint8_t*>(p.x) + first * kElt;
+    if (p.cols % 8 == 0) {
+      constexpr int kPer = 16 / kElt, kGroups = kMxTile / kPer, kStep = C::kThreads / kGroups;
+      const int g = tid % kGroups, r = tid / kGroups;
+      const bool in = g * kPer < cols;
+      const uint8_t* at = src + (static_cast<long long>(r) * p.cols + g * kPer) * kElt;
+      const long long step = static_cast<long long>(kStep) * p.cols * kElt;
 #pragma unroll
-    for (int i = 0; i < kEach; ++i) {
-      const int lr = i * (C::kThreads / kGroups) + static_cast<int>(threadIdx.x) / kGroups;
-      const int row = T.r0 + lr;
-      const bool exists = row < p.rows && n > 0;
-      const long long e = exists ? (static_cast<long long>(T.mat) * p.rows + row) * p.cols + col : 0;
-      copy16_async(tile + lr * C::kRowBytes + 16 * swizzled_group(lr, g),
-                   static_cast<const uint8_t*>(p.x) + e * kElt, exists);
+      for (int i = 0; i < kMxTile / kStep; ++i) {
+        const int lr = r + i * kStep;
+        const bool exists = in && lr < rows;
+        copy16_async(tile + lr * C::kRowBytes + 16 * swizzled_group(lr, g), exists ? at : p.x, exists);
+        at += step;
+      }
+      return;
+    }
+    constexpr int kPer = 4 / kElt;
+    if (p.cols % kPer == 0) {
+      constexpr int kWords = kMxTile / kPer, kStep = C::kThreads / kWords;
+      const int c = tid % kWords * kPer, r = tid / kWords;
+      const bool in = c < cols;
+      const uint8_t* at = src + (static_cast<long long>(r) * p.cols + c) * kElt;
+      const long long step = static_cast<long long>(kStep) * p.cols * kElt;
+#pragma unroll 8
+      for (int i = 0; i < kMxTile / kStep; ++i) {
+        const int lr = r + i * kStep;
+        const bool exists = in && lr < rows;
+        copy4_async(tile + lr * C::kRowBytes + tile_offset<C::kHalf>(lr, c), exists ? at : p.x, exists);
+        at += step;
+      }
+      return;
+    }
+  } else if (p.cols % 8 == 0) {   // four averages and four parameters at a time
+    constexpr int kGroups = kMxTile / 4, kStep = C::kThreads / kGroups;
+    const int g = tid % kGroups, r = tid / kGroups;
+    const bool in = g * 4 < cols;
+#pragma unroll 4
+    for (int i = 0; i < kMxTile / kStep; ++i) {
+      const int lr = r + i * kStep;
+      const long long e = first + static_cast<long long>(lr) * p.cols + g * 4;
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (in && lr < rows) {
+        const float4 m = *reinterpret_cast<const float4*>(p.ema + e);
+        float4 th;
+        if (C::kBf16) {
+          const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(p.x) + e);
+          th = make_float4(bf16_lo_f(w.x), bf16_hi_f(w.x), bf16_lo_f(w.y), bf16_hi_f(w.y));
+        } else {
+          th = *reinterpret_cast<const float4*>(static_cast<const float*>(p.x) + e);
+        }
+        v.x = fmaf(p.w_final, th.x, __fmul_rn(p.w_ema, m.x));
+        v.y = fmaf(p.w_final, th.y, __fmul_rn(p.w_ema, m.y));
+        v.z = fmaf(p.w_final, th.z, __fmul_rn(p.w_ema, m.z));
+        v.w = fmaf(p.w_final, th.w, __fmul_rn(p.w_ema, m.w));
+      }
+      *reinterpret_cast<float4*>(tile + lr * C::kRowBytes + 16 * swizzled_group(lr, g)) = v;
     }
     return;
   }
-#pragma unroll 4
-  for (int i = 0; i < kEach; ++i) {
-    const int lr = i * (C::kThreads / kGroups) + static_cast<int>(threadIdx.x) / kGroups;
-    const int row = T.r0 + lr;
-    const long long e = (static_cast<long long>(T.mat) * p.rows + row) * p.cols + col;
-    float v[kPer];
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) v[j] = 0.0f;
-    if (row < p.rows && n > 0) {
-      if (vec) {   // only the blend comes here: four fp32 averages and four parameters
-        const float4 a = *reinterpret_cast<const float4*>(p.ema + e);
-        const float em[4] = {a.x, a.y, a.z, a.w};
-        float th[4];
-        if (C::kBf16) {
-          const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(p.x) + e);
-          th[0] = bf16_lo_f(w.x); th[1] = bf16_hi_f(w.x); th[2] = bf16_lo_f(w.y); th[3] = bf16_hi_f(w.y);
-        } else {
-          const float4 f = *reinterpret_cast<const float4*>(static_cast<const float*>(p.x) + e);
-          th[0] = f.x; th[1] = f.y; th[2] = f.z; th[3] = f.w;
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] = fmaf(p.w_final, th[j], __fmul_rn(p.w_ema, em[j]));
-      } else {
-#pragma unroll
-        for (int j = 0; j < kPer; ++j) {
-          if (j < n) {
-            v[j] = load1t<C::kBf16>(p.x, e + j);
-            if (C::kBlend) v[j] = fmaf(p.w_final, v[j], __fmul_rn(p.w_ema, p.ema[e + j]));
-          }
-        }
-      }
+  constexpr int kStep = C::kThreads / kMxTile;
+  const int c = tid % kMxTile, r = tid / kMxTile;
+#pragma unroll 8
+  for (int i = 0; i < kMxTile / kStep; ++i) {
+    const int lr = r + i * kStep;
+    const long long e = first + static_cast<long long>(lr) * p.cols + c;
+    float v = 0.0f;
+    if (c < cols && lr < rows) {
+      v = load1t<C::kBf16>(p.x, e);
+      if constexpr (C::kBlend) v = fmaf(p.w_final, v, __fmul_rn(p.w_ema, p.ema[e]));
     }
-    uint8_t* at = tile + lr * C::kRowBytes + 16 * swizzled_group(lr, g);
-    if (C::kHalf)
-      *reinterpret_cast<uint4*>(at) =
-          make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4 % kPer], v[5 % kPer]),
-                     pack_bf16x2(v[6 % kPer], v[7 % kPer]));
+    uint8_t* at = tile + lr * C::kRowBytes + tile_offset<C::kHalf>(lr, c);
+    if constexpr (C::kHalf)
+      *reinterpret_cast<__nv_bfloat16*>(at) = __float2bfloat16_rn(v);   // exact: v is a bf16 value
     else
-      *reinterpret_cast<float4*>(at) = make_float4(v[0], v[1], v[2], v[3]);
+      *reinterpret_cast<float*>(at) = v;
   }
 }
 
-// Eight values of group cg (8 columns) of a tile row.
+// Eight neighbouring values of a tile row: four words of bf16 pairs, or eight
+// of fp32.
 template <bool kHalf>
-__device__ __forceinline__ void tile8(const uint8_t* row, int lr, int cg, float (&v)[8]) {
-  if (kHalf) {
-    const uint4 w = *reinterpret_cast<const uint4*>(row + 16 * swizzled_group(lr, cg));
-    const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-    for (int h = 0; h < 4; ++h) {
-      v[2 * h] = bf16_lo_f(ww[h]);
-      v[2 * h + 1] = bf16_hi_f(ww[h]);
-    }
-  } else {
-    const float4 a = *reinterpret_cast<const float4*>(row + 16 * swizzled_group(lr, 2 * cg));
-    const float4 b = *reinterpret_cast<const float4*>(row + 16 * swizzled_group(lr, 2 * cg + 1));
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+struct Eight {
+  uint32_t w[kHalf ? 4 : 8];
+
+  __device__ __forceinline__ float operator[](int j) const {
+    return kHalf ? ((j & 1) ? bf16_hi_f(w[j >> 1]) : bf16_lo_f(w[j >> 1])) : __uint_as_float(w[kHalf ? 0 : j]);
   }
-}
+
+  __device__ __forceinline__ void load(const uint8_t* row, int lr, int cg) {
+#pragma unroll
+    for (int h = 0; h < (kHalf ? 1 : 2); ++h) {
+      const uint4 x = *reinterpret_cast<const uint4*>(row + 16 * swizzled_group(lr, kHalf ? cg : 2 * cg + h));
+      w[4 * h] = x.x; w[4 * h + 1] = x.y; w[4 * h + 2] = x.z; w[4 * h + 3] = x.w;
+    }
+  }
+
+  __device__ __forceinline__ void store(uint8_t* row, int lr, int cg) const {
+#pragma unroll
+    for (int h = 0; h < (kHalf ? 1 : 2); ++h)
+      *reinterpret_cast<uint4*>(row + 16 * swizzled_group(lr, kHalf ? cg : 2 * cg + h)) =
+          make_uint4(w[4 * h], w[4 * h + 1], w[4 * h + 2], w[4 * h + 3]);
+  }
+
+  // Zeroes the elements whose 16-bit number is below the threshold (given in
+  // the upper half word). A number in an upper half word is compared in place.
+  __device__ __forceinline__ void drop(const uint4& u, uint32_t threshold_hi) {
+    const uint32_t uu[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const bool lo = (uu[j] << 16) >= threshold_hi, hi = uu[j] >= threshold_hi;
+      if (kHalf) {
+        w[j] &= (lo ? 0xFFFFu : 0u) | (hi ? 0xFFFF0000u : 0u);
+      } else {
+        w[kHalf ? 0 : 2 * j] = lo ? w[kHalf ? 0 : 2 * j] : 0u;
+        w[kHalf ? 0 : 2 * j + 1] = hi ? w[kHalf ? 0 : 2 * j + 1] : 0u;
+      }
+    }
+  }
+
+  // Largest magnitude over the four lanes that hold a block (NaN if any is).
+  __device__ __forceinline__ float block_amax() const {
+    if (kHalf) {
+      uint32_t m = max_abs_bf16x2(max_abs_bf16x2(w[0], w[1]), max_abs_bf16x2(w[2], w[3]));
+      m = max_abs_bf16x2(m, __shfl_xor_sync(0xffffffffu, m, 1));
+      m = max_abs_bf16x2(m, __shfl_xor_sync(0xffffffffu, m, 2));
+      return max_nan(bf16_lo_f(m), bf16_hi_f(m));
+    }
+    float m = fabsf((*this)[0]);
+#pragma unroll
+    for (int j = 1; j < 8; ++j) m = max_nan(m, fabsf((*this)[j]));
+    m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    return max_nan(m, __shfl_xor_sync(0xffffffffu, m, 2));
+  }
+
+  // The values in e2m1's range. mul, the dropout factor, and inv are applied
+  // one after the other: the first product is rounded, the second is exact
+  // (and so is the product of bf16 pairs with a power of two).
+  template <bool kMul>
+  __device__ __forceinline__ void scaled(float mul, float inv, float (&y)[8]) const {
+    if (kHalf && !kMul) {
+      const uint32_t inv2 = bf16_bits(inv) * 0x10001u;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t v = mul_bf16x2(w[j], inv2);
+        y[2 * j] = bf16_lo_f(v);
+        y[2 * j + 1] = bf16_hi_f(v);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) y[j] = kMul ? (*this)[j] * mul * inv : (*this)[j] * inv;
+    }
+  }
+};
 
 // Rows: 16 lanes per row, four lanes per block of 32 columns.
 template <int kSrc, bool kDrop, bool kStoch>
 __device__ __forceinline__ void code_rows(const QuantParams& p, uint8_t* tile, uint8_t* srow, const QuantTile& T,
                                           const RngKey& key) {
   using C = QuantConfig<kSrc>;
-  const int tid = threadIdx.x, cg = tid & 15, col = T.c0 + cg * 8;
+  constexpr int kStep = C::kThreads / 16;
+  const int tid = threadIdx.x, cg = tid & 15, r = tid >> 4, col = T.c0 + cg * 8;
   const float mul = kDrop ? p.scale : 1.0f;
+  const uint32_t group = static_cast<uint32_t>(col >> 3), threshold_hi = p.threshold << 16;
+  const int pitch = p.blocks_c * 16, rows = (col >> 5) < p.blocks_c ? p.rows - T.r0 : 0;
+  const uint32_t grow0 = static_cast<uint32_t>(T.mat) * static_cast<uint32_t>(p.rows) + static_cast<uint32_t>(T.r0);
+  uint8_t* out = p.q + static_cast<long long>(grow0 + r) * pitch + (col >> 1);
+  uint8_t* row = tile + r * C::kRowBytes;
 #pragma unroll 2
-  for (int i = 0; i < kMxTile * 16 / C::kThreads; ++i) {
-    const int lr = i * (C::kThreads / 16) + (tid >> 4), row = T.r0 + lr;
-    uint8_t* at = tile + lr * C::kRowBytes;
-    float v[8];
-    tile8<C::kHalf>(at, lr, cg, v);
-    const uint32_t grow = static_cast<uint32_t>(T.mat) * static_cast<uint32_t>(p.rows) + static_cast<uint32_t>(row);
+  for (int i = 0; i < kMxTile / kStep; ++i) {
+    const int lr = r + i * kStep;
+    Eight<C::kHalf> v;
+    v.load(row, lr, cg);
     if (kDrop) {
-      const uint4 u = philox8(key, kRngDropout, grow, static_cast<uint32_t>(col >> 3));
-      const uint32_t uu[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (((j & 1) ? uu[j >> 1] >> 16 : uu[j >> 1] & 0xFFFFu) < p.threshold) v[j] = 0.0f;
-      if (p.qt) {  // the column pass reads the masked values
-        if (C::kHalf) {
-          *reinterpret_cast<uint4*>(at + 16 * swizzled_group(lr, cg)) =
-              make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
-                         pack_bf16x2(v[6], v[7]));
-        } else {
-          *reinterpret_cast<float4*>(at + 16 * swizzled_group(lr, 2 * cg)) = make_float4(v[0], v[1], v[2], v[3]);
-          *reinterpret_cast<float4*>(at + 16 * swizzled_group(lr, 2 * cg + 1)) = make_float4(v[4], v[5], v[6], v[7]);
-        }
-      }
-      if (!p.q) continue;
+      v.drop(philox8(key, kRngDropout, grow0 + lr, group), threshold_hi);
+      if (p.qt) v.store(row, lr, cg);   // the column pass reads the masked values
     }
-    float amax = fabsf(v[0]);
-#pragma unroll
-    for (int j = 1; j < 8; ++j) amax = max_nan(amax, fabsf(v[j]));
-    amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-    amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-    float inv;
-    const uint32_t byte = block_scale(amax * mul, inv);
-    uint32_t w = kStoch ? code8_stochastic(v, mul, inv, philox8(key, kRngRows, grow, static_cast<uint32_t>(col >> 3)))
-                        : code8<kDrop>(v, mul, inv);
+    row += kStep * C::kRowBytes;
+    if (kDrop && !p.q) continue;
+    float inv, y[8];
+    const uint32_t byte = block_scale(v.block_amax() * mul, inv);
+    v.template scaled<kDrop>(mul, inv, y);
+    uint32_t w = kStoch ? pack8_stochastic(y, philox8(key, kRngRows, grow0 + lr, group)) : pack8_e2m1(y);
     if (byte == 255u) w = 0u;
     if ((tid & 3) == 0) srow[(lr & 31) * 16 + (lr >> 5) * 4 + (cg >> 2)] = static_cast<uint8_t>(byte);
-    if (row < p.rows && (col >> 5) < p.blocks_c) {
-      const long long qrow = static_cast<long long>(T.mat) * p.rows + row;
-      *reinterpret_cast<uint32_t*>(p.q + qrow * (p.blocks_c * 16) + (col >> 1)) = w;
-    }
+    if (lr < rows) *reinterpret_cast<uint32_t*>(out) = w;
+    out += kStep * pitch;
   }
 }
 
@@ -281,46 +369,59 @@ __device__ __forceinline__ void code_cols(const QuantParams& p, const uint8_t* t
   const int rb = lane >> 3;
   const int lc = (warp * 8 + (lane & 7)) * kCols;
   const float mul = kDrop ? p.scale : 1.0f;
-  const uint8_t* base = tile + rb * 32 * C::kRowBytes;
+  const uint8_t* at = tile + rb * 32 * C::kRowBytes + tile_offset<C::kHalf>(rb * 32, lc);
   uint32_t raw[32];
+#pragma unroll
+  for (int i = 0; i < 32; ++i) raw[i] = *reinterpret_cast<const uint32_t*>(at + i * C::kRowBytes);
+  float amax[kCols], inv[kCols];
   if (C::kHalf) {
-    const uint8_t* at = base + 16 * swizzled_group(rb * 32, lc >> 3) + (lc & 7) * 2;
+    uint32_t m[4] = {raw[0], raw[1], raw[2], raw[3]};
 #pragma unroll
-    for (int i = 0; i < 32; ++i) raw[i] = *reinterpret_cast<const uint32_t*>(at + i * C::kRowBytes);
+    for (int i = 4; i < 32; ++i) m[i & 3] = max_abs_bf16x2(m[i & 3], raw[i]);
+    const uint32_t all = max_abs_bf16x2(max_abs_bf16x2(m[0], m[1]), max_abs_bf16x2(m[2], m[3]));
+    amax[0] = bf16_lo_f(all);
+    amax[kCols - 1] = bf16_hi_f(all);
   } else {
-    const uint8_t* at = base + 16 * swizzled_group(rb * 32, lc >> 2) + (lc & 3) * 4;
+    float m[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int i = 0; i < 32; ++i) raw[i] = *reinterpret_cast<const uint32_t*>(at + i * C::kRowBytes);
+    for (int i = 0; i < 32; ++i) m[i & 3] = max_nan(m[i & 3], fabsf(__uint_as_float(raw[i])));
+    amax[0] = max_nan(max_nan(m[0], m[1]), max_nan(m[2], m[3]));
   }
+  uint32_t byte[kCols];
+#pragma unroll
+  for (int h = 0; h < kCols; ++h) {
+    byte[h] = block_scale(amax[h] * mul, inv[h]);
+    scol[((lc + h) & 31) * 16 + ((lc + h) >> 5) * 4 + rb] = static_cast<uint8_t>(byte[h]);
+  }
+  if (C::kHalf && !kDrop) {
+    const uint32_t inv2 = bf16_bits(inv[0]) | bf16_bits(inv[kCols - 1]) << 16;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) raw[i] = mul_bf16x2(raw[i], inv2);
+  }
+  const int block = (T.r0 >> 5) + rb;
 #pragma unroll
   for (int h = 0; h < kCols; ++h) {
     const int c = T.c0 + lc + h;
-    auto value = [&](int i) {
-      return C::kHalf ? (h ? bf16_hi_f(raw[i]) : bf16_lo_f(raw[i])) : __uint_as_float(raw[i]);
-    };
-    float amax = fabsf(value(0));
-#pragma unroll
-    for (int i = 1; i < 32; ++i) amax = max_nan(amax, fabsf(value(i)));
-    float inv;
-    const uint32_t byte = block_scale(amax * mul, inv);
-    scol[((lc + h) & 31) * 16 + ((lc + h) >> 5) * 4 + rb] = static_cast<uint8_t>(byte);
     const uint32_t gcol = static_cast<uint32_t>(T.mat) * static_cast<uint32_t>(p.cols) + static_cast<uint32_t>(c);
     uint32_t w[4];
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
-      float v[8];
+      float y[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = value(g * 8 + j);
-      w[g] = kStoch ? code8_stochastic(v, mul, inv, philox8(key, kRngCols, gcol,
-                                                            static_cast<uint32_t>((T.r0 >> 3) + rb * 4 + g)))
-                    : code8<kDrop>(v, mul, inv);
-      if (byte == 255u) w[g] = 0u;
+      for (int j = 0; j < 8; ++j) {
+        const uint32_t x = raw[g * 8 + j];
+        y[j] = C::kHalf ? (h ? bf16_hi_f(x) : bf16_lo_f(x)) : __uint_as_float(x);
+        if (kDrop) y[j] *= mul;
+        if (kDrop || !C::kHalf) y[j] *= inv[h];
+      }
+      w[g] = kStoch ? pack8_stochastic(y, philox8(key, kRngCols, gcol,
+                                                  static_cast<uint32_t>((T.r0 >> 3) + rb * 4 + g)))
+                    : pack8_e2m1(y);
+      if (byte[h] == 255u) w[g] = 0u;
     }
-    const int block = (T.r0 >> 5) + rb;
-    if (c < p.cols && block < p.blocks_r) {
-      const long long qrow = static_cast<long long>(T.mat) * p.cols + c;
-      *reinterpret_cast<uint4*>(p.qt + (qrow * p.blocks_r + block) * 16) = make_uint4(w[0], w[1], w[2], w[3]);
-    }
+    if (c < p.cols && block < p.blocks_r)
+      *reinterpret_cast<uint4*>(p.qt + (static_cast<long long>(gcol) * p.blocks_r + block) * 16) =
+          make_uint4(w[0], w[1], w[2], w[3]);
   }
 }
 
@@ -434,31 +535,34 @@ __device__ __forceinline__ uint32_t scale_at(const DequantParams& p, int mat, in
   return p.s[t * kMxTileBytes + (row & 31) * 16 + ((row & 127) >> 5) * 4 + (block & 3)];
 }
 
-// Rows whose length is a multiple of 8: four groups of eight elements per
-// thread, all loads first.
+// Rows whose length is a multiple of 8: one block per 128 x 128 tile, eight
+// groups of 8 elements per thread, all in one column of groups: rows 16 apart.
+// The scales of rows r, r + 32, .. of a tile share 16 bytes, so two loads
+// bring all eight.
 template <bool kBf16>
 __global__ void __launch_bounds__(256) dequantize_kernel(const __grid_constant__ DequantParams p) {
-  constexpr int kEach = 4;
-  const uint32_t i0 = blockIdx.x * (256u * kEach) + threadIdx.x;
-  uint32_t w[kEach], byte[kEach];
+  const int per_mat = p.tiles_r * p.tiles_c;
+  const int mat = static_cast<int>(blockIdx.x) / per_mat, t = static_cast<int>(blockIdx.x) - mat * per_mat;
+  const int tr = t / p.tiles_c, tc = t - tr * p.tiles_c;
+  const int cg = threadIdx.x & 15, r = threadIdx.x >> 4, col = tc * kMxTile + cg * 8;
+  const int rows = col < p.cols ? p.rows - tr * kMxTile : 0;
+  const uint4* st = reinterpret_cast<const uint4*>(p.s + static_cast<long long>(blockIdx.x) * kMxTileBytes);
+  const uint4 sa = st[r], sb = st[r + 16];
+  const uint32_t scale[8] = {sa.x, sb.x, sa.y, sb.y, sa.z, sb.z, sa.w, sb.w};   // row r + 16 i
+  const long long row0 = static_cast<long long>(mat) * p.rows + tr * kMxTile + r;
+  const int pitch = p.blocks * 16, shift = (cg >> 2) * 8;
+  const uint8_t* in = p.q + row0 * pitch + (col >> 1);
+  uint32_t w[8];
 #pragma unroll
-  for (int u = 0; u < kEach; ++u) {
-    const uint32_t i = i0 + u * 256u;
-    if (i < p.total) {
-      const int grow = fdiv(static_cast<int>(i), p.fd_groups);
-      const int g = static_cast<int>(i) - grow * p.groups;
-      const int mat = fdiv(grow, p.fd_rows), row = grow - mat * p.rows;
-      w[u] = *reinterpret_cast<const uint32_t*>(p.q + static_cast<long long>(grow) * p.blocks * 16 + g * 4);
-      byte[u] = scale_at(p, mat, row, g >> 2);
-    }
-  }
+  for (int i = 0; i < 8; ++i)
+    if (r + 16 * i < rows) w[i] = *reinterpret_cast<const uint32_t*>(in + i * 16 * pitch);
+  const long long out = row0 * p.cols + col;
 #pragma unroll
-  for (int u = 0; u < kEach; ++u) {
-    const uint32_t i = i0 + u * 256u;
-    if (i < p.total) {
+  for (int i = 0; i < 8; ++i) {
+    if (r + 16 * i < rows) {
       float v[8];
-      decode8(w[u], byte[u], v);
-      store8t<kBf16>(p.out, static_cast<long long>(i) * 8, v);
+      decode8(w[i], (scale[i] >> shift) & 255u, v);
+      store8t<kBf16>(p.out, out + static_cast<long long>(16 * i) * p.cols, v);
     }
   }
 }
@@ -501,7 +605,7 @@ cudaError_t launch_dequantize(const DequantParams& p, bool bf16, int sms, cudaSt
   const uint32_t want = (p.total + 255) / 256, most = 32u * static_cast<uint32_t>(sms);
   const uint32_t grid = want < most ? want : most;
   if (p.cols % 8 == 0) {
-    const uint32_t blocks = (p.total + 1023) / 1024;
+    const uint32_t blocks = static_cast<uint32_t>(p.count) * p.tiles_r * p.tiles_c;
     if (bf16) dequantize_kernel<true><<<blocks, 256, 0, s>>>(p);
     else dequantize_kernel<false><<<blocks, 256, 0, s>>>(p);
   } else {

@@ -35,6 +35,20 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void*
       : "memory");
 }
 
+// Non-blocking: has the barrier phase of `parity` completed (cluster-scope
+// acquire)?
+__device__ __forceinline__ bool mbar_test_cluster(const uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
 // D[tmem] (+)= (A scaled) (B scaled)^T: e2m1 operands in shared memory, one
 // e8m0 scale per 32 elements of K in TMEM, K = 64.
 __device__ __forceinline__ void umma_mxf4(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
