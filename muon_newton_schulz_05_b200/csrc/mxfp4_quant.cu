@@ -10,9 +10,8 @@
 //
 // quantize: persistent blocks take 128 x 128 tiles, read each once (cp.async,
 // the next tiles in flight while one is coded) and write both orientations
-// from shared memory, each with its whole 512-byte scale tile. Rows are coded
-// by four lanes per block of 32 columns, columns by one thread per 32-row
-// block. Dropout is applied in the row pass, which writes the masked values
+// from shared memory, each with its whole 512-byte scale tile. A thread codes
+// whole blocks, along a row or down a column. Dropout is applied in the row pass, which writes the masked values
 // back for the column pass; the blend of the parameters with their average is
 // formed while the tile is filled.
 #include "dtype_io.cuh"
@@ -24,6 +23,12 @@ namespace muon {
 __device__ __forceinline__ float max_nan(float a, float b) {
   float r;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+__device__ __forceinline__ float max_nan(float a, float b, float c) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
 
@@ -89,9 +94,15 @@ __device__ __forceinline__ uint32_t max_abs_bf16x2(uint32_t a, uint32_t b) {
   return r;
 }
 
-__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("mul.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+// Both halves of w as fp32, times those of f (exact where f's are powers of
+// two; adding -0 keeps the sign of a zero). One instruction each, and not on
+// the pipe that the conversions and maxima keep busy.
+__device__ __forceinline__ float2 mul_bf16x2_f32(uint32_t w, uint32_t f) {
+  float2 r;
+  asm("{\n\t.reg .b16 a, b, c, d;\n\tmov.b32 {a, b}, %2;\n\tmov.b32 {c, d}, %3;\n\t"
+      "fma.rn.f32.bf16 %0, a, c, 0f80000000;\n\tfma.rn.f32.bf16 %1, b, d, 0f80000000;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "r"(w), "r"(f));
   return r;
 }
 
@@ -247,114 +258,114 @@ __device__ __forceinline__ void fill_tile(const QuantParams& p, uint8_t* tile, c
   }
 }
 
-// Eight neighbouring values of a tile row: four words of bf16 pairs, or eight
-// of fp32.
-template <bool kHalf>
-struct Eight {
-  uint32_t w[kHalf ? 4 : 8];
-
-  __device__ __forceinline__ float operator[](int j) const {
-    return kHalf ? ((j & 1) ? bf16_hi_f(w[j >> 1]) : bf16_lo_f(w[j >> 1])) : __uint_as_float(w[kHalf ? 0 : j]);
-  }
-
-  __device__ __forceinline__ void load(const uint8_t* row, int lr, int cg) {
+// Largest magnitude of 32 fp32 values (NaN if any is).
+__device__ __forceinline__ float amax32(const uint32_t (&w)[32]) {
+  float m[2] = {fabsf(__uint_as_float(w[0])), fabsf(__uint_as_float(w[1]))};
 #pragma unroll
-    for (int h = 0; h < (kHalf ? 1 : 2); ++h) {
-      const uint4 x = *reinterpret_cast<const uint4*>(row + 16 * swizzled_group(lr, kHalf ? cg : 2 * cg + h));
-      w[4 * h] = x.x; w[4 * h + 1] = x.y; w[4 * h + 2] = x.z; w[4 * h + 3] = x.w;
-    }
-  }
+  for (int i = 2; i < 32; i += 2)
+    m[(i >> 1) & 1] = max_nan(m[(i >> 1) & 1], fabsf(__uint_as_float(w[i])), fabsf(__uint_as_float(w[i + 1])));
+  return max_nan(m[0], m[1]);
+}
 
-  __device__ __forceinline__ void store(uint8_t* row, int lr, int cg) const {
-#pragma unroll
-    for (int h = 0; h < (kHalf ? 1 : 2); ++h)
-      *reinterpret_cast<uint4*>(row + 16 * swizzled_group(lr, kHalf ? cg : 2 * cg + h)) =
-          make_uint4(w[4 * h], w[4 * h + 1], w[4 * h + 2], w[4 * h + 3]);
-  }
-
-  // Zeroes the elements whose 16-bit number is below the threshold (given in
-  // the upper half word). A number in an upper half word is compared in place.
-  __device__ __forceinline__ void drop(const uint4& u, uint32_t threshold_hi) {
-    const uint32_t uu[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const bool lo = (uu[j] << 16) >= threshold_hi, hi = uu[j] >= threshold_hi;
-      if (kHalf) {
-        w[j] &= (lo ? 0xFFFFu : 0u) | (hi ? 0xFFFF0000u : 0u);
-      } else {
-        w[kHalf ? 0 : 2 * j] = lo ? w[kHalf ? 0 : 2 * j] : 0u;
-        w[kHalf ? 0 : 2 * j + 1] = hi ? w[kHalf ? 0 : 2 * j + 1] : 0u;
-      }
-    }
-  }
-
-  // Largest magnitude over the four lanes that hold a block (NaN if any is).
-  __device__ __forceinline__ float block_amax() const {
-    if (kHalf) {
-      uint32_t m = max_abs_bf16x2(max_abs_bf16x2(w[0], w[1]), max_abs_bf16x2(w[2], w[3]));
-      m = max_abs_bf16x2(m, __shfl_xor_sync(0xffffffffu, m, 1));
-      m = max_abs_bf16x2(m, __shfl_xor_sync(0xffffffffu, m, 2));
-      return max_nan(bf16_lo_f(m), bf16_hi_f(m));
-    }
-    float m = fabsf((*this)[0]);
-#pragma unroll
-    for (int j = 1; j < 8; ++j) m = max_nan(m, fabsf((*this)[j]));
-    m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 1));
-    return max_nan(m, __shfl_xor_sync(0xffffffffu, m, 2));
-  }
-
-  // The values in e2m1's range. mul, the dropout factor, and inv are applied
-  // one after the other: the first product is rounded, the second is exact
-  // (and so is the product of bf16 pairs with a power of two).
-  template <bool kMul>
-  __device__ __forceinline__ void scaled(float mul, float inv, float (&y)[8]) const {
-    if (kHalf && !kMul) {
-      const uint32_t inv2 = bf16_bits(inv) * 0x10001u;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint32_t v = mul_bf16x2(w[j], inv2);
-        y[2 * j] = bf16_lo_f(v);
-        y[2 * j + 1] = bf16_hi_f(v);
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) y[j] = kMul ? (*this)[j] * mul * inv : (*this)[j] * inv;
-    }
-  }
-};
-
-// Rows: 16 lanes per row, four lanes per block of 32 columns.
+// Rows: a thread codes one block of 32 columns. It reads the block's four
+// groups of 8 elements in an order that differs between neighbouring lanes
+// (group j is the block's j ^ order), so that their loads fall into different
+// banks, and puts the four words of codes back in order at the end.
 template <int kSrc, bool kDrop, bool kStoch>
 __device__ __forceinline__ void code_rows(const QuantParams& p, uint8_t* tile, uint8_t* srow, const QuantTile& T,
                                           const RngKey& key) {
   using C = QuantConfig<kSrc>;
-  constexpr int kStep = C::kThreads / 16;
-  const int tid = threadIdx.x, cg = tid & 15, r = tid >> 4, col = T.c0 + cg * 8;
+  constexpr int kWords = C::kHalf ? 16 : 32, kPer = kWords / 4;   // 32-bit words per block and per group
+  const int tid = threadIdx.x, blk = tid & 3;
   const float mul = kDrop ? p.scale : 1.0f;
-  const uint32_t group = static_cast<uint32_t>(col >> 3), threshold_hi = p.threshold << 16;
-  const int pitch = p.blocks_c * 16, rows = (col >> 5) < p.blocks_c ? p.rows - T.r0 : 0;
+  const uint32_t threshold_hi = p.threshold << 16;
+  const int block = (T.c0 >> 5) + blk;
+  const int rows = block < p.blocks_c ? p.rows - T.r0 : 0;
   const uint32_t grow0 = static_cast<uint32_t>(T.mat) * static_cast<uint32_t>(p.rows) + static_cast<uint32_t>(T.r0);
-  uint8_t* out = p.q + static_cast<long long>(grow0 + r) * pitch + (col >> 1);
-  uint8_t* row = tile + r * C::kRowBytes;
-#pragma unroll 2
-  for (int i = 0; i < kMxTile / kStep; ++i) {
-    const int lr = r + i * kStep;
-    Eight<C::kHalf> v;
-    v.load(row, lr, cg);
-    if (kDrop) {
-      v.drop(philox8(key, kRngDropout, grow0 + lr, group), threshold_hi);
-      if (p.qt) v.store(row, lr, cg);   // the column pass reads the masked values
+#pragma unroll
+  for (int i = 0; i < kMxTile * 4 / C::kThreads; ++i) {
+    const int lr = (tid >> 2) + i * (C::kThreads / 4);
+    const uint32_t order = static_cast<uint32_t>((blk >> 1) | ((lr & 1) << 1));
+    uint8_t* row = tile + lr * C::kRowBytes;
+    uint32_t w[kWords];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int g8 = blk * 4 + static_cast<int>(j ^ order);
+#pragma unroll
+      for (int h = 0; h < kPer / 4; ++h) {
+        const uint4 x = *reinterpret_cast<const uint4*>(row + 16 * swizzled_group(lr, C::kHalf ? g8 : 2 * g8 + h));
+        w[j * kPer + 4 * h] = x.x; w[j * kPer + 4 * h + 1] = x.y;
+        w[j * kPer + 4 * h + 2] = x.z; w[j * kPer + 4 * h + 3] = x.w;
+      }
     }
-    row += kStep * C::kRowBytes;
-    if (kDrop && !p.q) continue;
-    float inv, y[8];
-    const uint32_t byte = block_scale(v.block_amax() * mul, inv);
-    v.template scaled<kDrop>(mul, inv, y);
-    uint32_t w = kStoch ? pack8_stochastic(y, philox8(key, kRngRows, grow0 + lr, group)) : pack8_e2m1(y);
-    if (byte == 255u) w = 0u;
-    if ((tid & 3) == 0) srow[(lr & 31) * 16 + (lr >> 5) * 4 + (cg >> 2)] = static_cast<uint8_t>(byte);
-    if (lr < rows) *reinterpret_cast<uint32_t*>(out) = w;
-    out += kStep * pitch;
+    if (kDrop) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int g8 = blk * 4 + static_cast<int>(j ^ order);
+        const uint4 u = philox8(key, kRngDropout, grow0 + lr, static_cast<uint32_t>((T.c0 >> 3) + g8));
+        const uint32_t uu[4] = {u.x, u.y, u.z, u.w};
+        // a number in an upper half word is compared where it is
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          const bool lo = (uu[t] << 16) >= threshold_hi, hi = uu[t] >= threshold_hi;
+          if (C::kHalf) {
+            w[j * kPer + t] &= (lo ? 0xFFFFu : 0u) | (hi ? 0xFFFF0000u : 0u);
+          } else {
+            if (!lo) w[j * kPer + (2 * t) % kPer] = 0u;
+            if (!hi) w[j * kPer + (2 * t + 1) % kPer] = 0u;
+          }
+        }
+        if (p.qt) {   // the column pass reads the masked values
+#pragma unroll
+          for (int h = 0; h < kPer / 4; ++h)
+            *reinterpret_cast<uint4*>(row + 16 * swizzled_group(lr, C::kHalf ? g8 : 2 * g8 + h)) =
+                make_uint4(w[j * kPer + 4 * h], w[j * kPer + 4 * h + 1], w[j * kPer + 4 * h + 2],
+                           w[j * kPer + 4 * h + 3]);
+        }
+      }
+      if (!p.q) continue;
+    }
+    float amax;
+    if constexpr (C::kHalf) {
+      uint32_t m = max_abs_bf16x2(w[0], w[1]);
+#pragma unroll
+      for (int t = 2; t < 16; ++t) m = max_abs_bf16x2(m, w[t]);
+      amax = max_nan(bf16_lo_f(m), bf16_hi_f(m));
+    } else {
+      amax = amax32(w);
+    }
+    float inv;
+    const uint32_t byte = block_scale(amax * mul, inv);
+    srow[(lr & 31) * 16 + (lr >> 5) * 4 + blk] = static_cast<uint8_t>(byte);
+    const uint32_t inv2 = bf16_bits(kDrop ? 1.0f : inv) * 0x10001u;
+    uint32_t c[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      float y[8];
+      if constexpr (C::kHalf) {
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          const float2 f = mul_bf16x2_f32(w[j * kPer + t], inv2);
+          y[2 * t] = f.x;
+          y[2 * t + 1] = f.y;
+        }
+      } else {
+#pragma unroll
+        for (int t = 0; t < 8; ++t) y[t] = __uint_as_float(w[j * kPer + t]) * (kDrop ? mul : inv);
+      }
+      if (kDrop) {   // the dropout factor and the scale one after the other: only the first product is rounded
+#pragma unroll
+        for (int t = 0; t < 8; ++t) y[t] = (C::kHalf ? y[t] * mul : y[t]) * inv;
+      }
+      const uint32_t g = static_cast<uint32_t>((T.c0 >> 3) + blk * 4) + (static_cast<uint32_t>(j) ^ order);
+      c[j] = kStoch ? pack8_stochastic(y, philox8(key, kRngRows, grow0 + lr, g)) : pack8_e2m1(y);
+      if (byte == 255u) c[j] = 0u;
+    }
+    const bool s0 = order & 1u, s1 = order & 2u;
+    const uint32_t a0 = s0 ? c[1] : c[0], a1 = s0 ? c[0] : c[1], a2 = s0 ? c[3] : c[2], a3 = s0 ? c[2] : c[3];
+    if (lr < rows)
+      *reinterpret_cast<uint4*>(p.q + (static_cast<long long>(grow0 + lr) * p.blocks_c + block) * 16) =
+          make_uint4(s1 ? a2 : a0, s1 ? a3 : a1, s1 ? a0 : a2, s1 ? a1 : a3);
   }
 }
 
@@ -374,18 +385,15 @@ __device__ __forceinline__ void code_cols(const QuantParams& p, const uint8_t* t
 #pragma unroll
   for (int i = 0; i < 32; ++i) raw[i] = *reinterpret_cast<const uint32_t*>(at + i * C::kRowBytes);
   float amax[kCols], inv[kCols];
-  if (C::kHalf) {
-    uint32_t m[4] = {raw[0], raw[1], raw[2], raw[3]};
+  if constexpr (C::kHalf) {
+    uint32_t m[2] = {raw[0], raw[1]};
 #pragma unroll
-    for (int i = 4; i < 32; ++i) m[i & 3] = max_abs_bf16x2(m[i & 3], raw[i]);
-    const uint32_t all = max_abs_bf16x2(max_abs_bf16x2(m[0], m[1]), max_abs_bf16x2(m[2], m[3]));
-    amax[0] = bf16_lo_f(all);
-    amax[kCols - 1] = bf16_hi_f(all);
+    for (int i = 2; i < 32; ++i) m[i & 1] = max_abs_bf16x2(m[i & 1], raw[i]);
+    m[0] = max_abs_bf16x2(m[0], m[1]);
+    amax[0] = bf16_lo_f(m[0]);
+    amax[1] = bf16_hi_f(m[0]);
   } else {
-    float m[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int i = 0; i < 32; ++i) m[i & 3] = max_nan(m[i & 3], fabsf(__uint_as_float(raw[i])));
-    amax[0] = max_nan(max_nan(m[0], m[1]), max_nan(m[2], m[3]));
+    amax[0] = amax32(raw);
   }
   uint32_t byte[kCols];
 #pragma unroll
@@ -393,36 +401,36 @@ __device__ __forceinline__ void code_cols(const QuantParams& p, const uint8_t* t
     byte[h] = block_scale(amax[h] * mul, inv[h]);
     scol[((lc + h) & 31) * 16 + ((lc + h) >> 5) * 4 + rb] = static_cast<uint8_t>(byte[h]);
   }
-  if (C::kHalf && !kDrop) {
-    const uint32_t inv2 = bf16_bits(inv[0]) | bf16_bits(inv[kCols - 1]) << 16;
+  const uint32_t inv2 = kDrop ? 0x3F803F80u : bf16_bits(inv[0]) | bf16_bits(inv[kCols - 1]) << 16;
+  const uint32_t gcol = static_cast<uint32_t>(T.mat) * static_cast<uint32_t>(p.cols) + static_cast<uint32_t>(T.c0 + lc);
+  uint32_t w[kCols][4];
 #pragma unroll
-    for (int i = 0; i < 32; ++i) raw[i] = mul_bf16x2(raw[i], inv2);
+  for (int g = 0; g < 4; ++g) {
+    float y[kCols][8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if constexpr (C::kHalf) {
+        const float2 f = mul_bf16x2_f32(raw[g * 8 + j], inv2);
+        y[0][j] = kDrop ? f.x * mul * inv[0] : f.x;
+        y[1][j] = kDrop ? f.y * mul * inv[1] : f.y;
+      } else {
+        y[0][j] = kDrop ? __uint_as_float(raw[g * 8 + j]) * mul * inv[0] : __uint_as_float(raw[g * 8 + j]) * inv[0];
+      }
+    }
+#pragma unroll
+    for (int h = 0; h < kCols; ++h) {
+      w[h][g] = kStoch ? pack8_stochastic(y[h], philox8(key, kRngCols, gcol + h,
+                                                        static_cast<uint32_t>((T.r0 >> 3) + rb * 4 + g)))
+                       : pack8_e2m1(y[h]);
+      if (byte[h] == 255u) w[h][g] = 0u;
+    }
   }
   const int block = (T.r0 >> 5) + rb;
 #pragma unroll
-  for (int h = 0; h < kCols; ++h) {
-    const int c = T.c0 + lc + h;
-    const uint32_t gcol = static_cast<uint32_t>(T.mat) * static_cast<uint32_t>(p.cols) + static_cast<uint32_t>(c);
-    uint32_t w[4];
-#pragma unroll
-    for (int g = 0; g < 4; ++g) {
-      float y[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const uint32_t x = raw[g * 8 + j];
-        y[j] = C::kHalf ? (h ? bf16_hi_f(x) : bf16_lo_f(x)) : __uint_as_float(x);
-        if (kDrop) y[j] *= mul;
-        if (kDrop || !C::kHalf) y[j] *= inv[h];
-      }
-      w[g] = kStoch ? pack8_stochastic(y, philox8(key, kRngCols, gcol,
-                                                  static_cast<uint32_t>((T.r0 >> 3) + rb * 4 + g)))
-                    : pack8_e2m1(y);
-      if (byte[h] == 255u) w[g] = 0u;
-    }
-    if (c < p.cols && block < p.blocks_r)
-      *reinterpret_cast<uint4*>(p.qt + (static_cast<long long>(gcol) * p.blocks_r + block) * 16) =
-          make_uint4(w[0], w[1], w[2], w[3]);
-  }
+  for (int h = 0; h < kCols; ++h)
+    if (T.c0 + lc + h < p.cols && block < p.blocks_r)
+      *reinterpret_cast<uint4*>(p.qt + (static_cast<long long>(gcol + h) * p.blocks_r + block) * 16) =
+          make_uint4(w[h][0], w[h][1], w[h][2], w[h][3]);
 }
 
 // Persistent over the tiles. While a tile is coded, the next ones are on their
