@@ -48,6 +48,7 @@ struct QuantParams {
   unsigned long long site;
   int count, rows, cols;
   int tiles_r, tiles_c;         // 128 x 128 tiles
+  FastDiv fd_tiles, fd_tiles_c; // by tiles_r * tiles_c, by tiles_c
   int blocks_r, blocks_c;       // 32-element blocks along the rows / columns
   uint32_t threshold;           // dropout; 0: none
   float scale;

@@ -107,6 +107,8 @@ muon_status run_quantize(QuantParams& q, int32_t dtype, int64_t count, int64_t r
   q.cols = static_cast<int>(cols);
   q.tiles_r = static_cast<int>(ceil_div(rows, kMxTile));
   q.tiles_c = static_cast<int>(ceil_div(cols, kMxTile));
+  q.fd_tiles = make_fastdiv(static_cast<uint32_t>(q.tiles_r) * static_cast<uint32_t>(q.tiles_c));
+  q.fd_tiles_c = make_fastdiv(static_cast<uint32_t>(q.tiles_c));
   q.blocks_r = static_cast<int>(ceil_div(rows, kMxBlock));
   q.blocks_c = static_cast<int>(ceil_div(cols, kMxBlock));
   return launch_quantize(q, dtype == MUON_BF16, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess

@@ -86,11 +86,10 @@ __device__ __forceinline__ uint32_t pack8_stochastic(const float (&y)[8], const 
   return w;
 }
 
+// Per half, the larger magnitude (NaN if either is); its sign means nothing.
 __device__ __forceinline__ uint32_t max_abs_bf16x2(uint32_t a, uint32_t b) {
   uint32_t r;
-  asm("{\n\t.reg .b32 x, y;\n\tabs.bf16x2 x, %1;\n\tabs.bf16x2 y, %2;\n\tmax.NaN.bf16x2 %0, x, y;\n\t}"
-      : "=r"(r)
-      : "r"(a), "r"(b));
+  asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
 
@@ -146,9 +145,9 @@ struct QuantTile {
 __device__ __forceinline__ QuantTile quant_tile(const QuantParams& p, int t) {
   const int per_mat = p.tiles_r * p.tiles_c;
   QuantTile x;
-  x.mat = t / per_mat;
+  x.mat = fdiv(t, p.fd_tiles);
   const int u = t - x.mat * per_mat;
-  const int tr = u / p.tiles_c, tc = u - tr * p.tiles_c;
+  const int tr = fdiv(u, p.fd_tiles_c), tc = u - tr * p.tiles_c;
   x.r0 = tr * kMxTile;
   x.c0 = tc * kMxTile;
   x.at = t;
@@ -216,25 +215,38 @@ __device__ __forceinline__ void fill_tile(const QuantParams& p, uint8_t* tile, c
     constexpr int kGroups = kMxTile / 4, kStep = C::kThreads / kGroups;
     const int g = tid % kGroups, r = tid / kGroups;
     const bool in = g * 4 < cols;
-#pragma unroll 4
-    for (int i = 0; i < kMxTile / kStep; ++i) {
+    constexpr int kEach = kMxTile / kStep;
+    float4 m[kEach];
+    uint4 th[kEach];   // four parameters: fp32, or bf16 in x and y
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
       const int lr = r + i * kStep;
       const long long e = first + static_cast<long long>(lr) * p.cols + g * 4;
-      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      m[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      th[i] = make_uint4(0u, 0u, 0u, 0u);
       if (in && lr < rows) {
-        const float4 m = *reinterpret_cast<const float4*>(p.ema + e);
-        float4 th;
+        m[i] = *reinterpret_cast<const float4*>(p.ema + e);
         if (C::kBf16) {
           const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(p.x) + e);
-          th = make_float4(bf16_lo_f(w.x), bf16_hi_f(w.x), bf16_lo_f(w.y), bf16_hi_f(w.y));
+          th[i].x = w.x;
+          th[i].y = w.y;
         } else {
-          th = *reinterpret_cast<const float4*>(static_cast<const float*>(p.x) + e);
+          th[i] = *reinterpret_cast<const uint4*>(static_cast<const float*>(p.x) + e);
         }
-        v.x = fmaf(p.w_final, th.x, __fmul_rn(p.w_ema, m.x));
-        v.y = fmaf(p.w_final, th.y, __fmul_rn(p.w_ema, m.y));
-        v.z = fmaf(p.w_final, th.z, __fmul_rn(p.w_ema, m.z));
-        v.w = fmaf(p.w_final, th.w, __fmul_rn(p.w_ema, m.w));
       }
+    }
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const int lr = r + i * kStep;
+      const float4 t = C::kBf16 ? make_float4(bf16_lo_f(th[i].x), bf16_hi_f(th[i].x), bf16_lo_f(th[i].y),
+                                              bf16_hi_f(th[i].y))
+                                : make_float4(__uint_as_float(th[i].x), __uint_as_float(th[i].y),
+                                              __uint_as_float(th[i].z), __uint_as_float(th[i].w));
+      float4 v;
+      v.x = fmaf(p.w_final, t.x, __fmul_rn(p.w_ema, m[i].x));
+      v.y = fmaf(p.w_final, t.y, __fmul_rn(p.w_ema, m[i].y));
+      v.z = fmaf(p.w_final, t.z, __fmul_rn(p.w_ema, m[i].z));
+      v.w = fmaf(p.w_final, t.w, __fmul_rn(p.w_ema, m[i].w));
       *reinterpret_cast<float4*>(tile + lr * C::kRowBytes + 16 * swizzled_group(lr, g)) = v;
     }
     return;
@@ -298,12 +310,17 @@ __device__ __forceinline__ void code_rows(const QuantParams& p, uint8_t* tile, u
         w[j * kPer + 4 * h + 2] = x.z; w[j * kPer + 4 * h + 3] = x.w;
       }
     }
+    uint32_t group[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      group[j] = static_cast<uint32_t>((T.c0 >> 3) + blk * 4) + (static_cast<uint32_t>(j) ^ order);
     if (kDrop) {
+      uint4 num[4];
+      philox8x4(key, kRngDropout, grow0 + lr, group, num);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int g8 = blk * 4 + static_cast<int>(j ^ order);
-        const uint4 u = philox8(key, kRngDropout, grow0 + lr, static_cast<uint32_t>((T.c0 >> 3) + g8));
-        const uint32_t uu[4] = {u.x, u.y, u.z, u.w};
+        const uint32_t uu[4] = {num[j].x, num[j].y, num[j].z, num[j].w};
         // a number in an upper half word is compared where it is
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
@@ -330,7 +347,7 @@ __device__ __forceinline__ void code_rows(const QuantParams& p, uint8_t* tile, u
       uint32_t m = max_abs_bf16x2(w[0], w[1]);
 #pragma unroll
       for (int t = 2; t < 16; ++t) m = max_abs_bf16x2(m, w[t]);
-      amax = max_nan(bf16_lo_f(m), bf16_hi_f(m));
+      amax = max_nan(fabsf(bf16_lo_f(m)), fabsf(bf16_hi_f(m)));
     } else {
       amax = amax32(w);
     }
@@ -339,6 +356,8 @@ __device__ __forceinline__ void code_rows(const QuantParams& p, uint8_t* tile, u
     srow[(lr & 31) * 16 + (lr >> 5) * 4 + blk] = static_cast<uint8_t>(byte);
     const uint32_t inv2 = bf16_bits(kDrop ? 1.0f : inv) * 0x10001u;
     uint32_t c[4];
+    uint4 num[4];
+    if (kStoch) philox8x4(key, kRngRows, grow0 + lr, group, num);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       float y[8];
@@ -357,8 +376,7 @@ __device__ __forceinline__ void code_rows(const QuantParams& p, uint8_t* tile, u
 #pragma unroll
         for (int t = 0; t < 8; ++t) y[t] = (C::kHalf ? y[t] * mul : y[t]) * inv;
       }
-      const uint32_t g = static_cast<uint32_t>((T.c0 >> 3) + blk * 4) + (static_cast<uint32_t>(j) ^ order);
-      c[j] = kStoch ? pack8_stochastic(y, philox8(key, kRngRows, grow0 + lr, g)) : pack8_e2m1(y);
+      c[j] = kStoch ? pack8_stochastic(y, num[j]) : pack8_e2m1(y);
       if (byte == 255u) c[j] = 0u;
     }
     const bool s0 = order & 1u, s1 = order & 2u;
@@ -390,8 +408,8 @@ __device__ __forceinline__ void code_cols(const QuantParams& p, const uint8_t* t
 #pragma unroll
     for (int i = 2; i < 32; ++i) m[i & 1] = max_abs_bf16x2(m[i & 1], raw[i]);
     m[0] = max_abs_bf16x2(m[0], m[1]);
-    amax[0] = bf16_lo_f(m[0]);
-    amax[1] = bf16_hi_f(m[0]);
+    amax[0] = fabsf(bf16_lo_f(m[0]));
+    amax[1] = fabsf(bf16_hi_f(m[0]));
   } else {
     amax[0] = amax32(raw);
   }
@@ -403,25 +421,27 @@ __device__ __forceinline__ void code_cols(const QuantParams& p, const uint8_t* t
   }
   const uint32_t inv2 = kDrop ? 0x3F803F80u : bf16_bits(inv[0]) | bf16_bits(inv[kCols - 1]) << 16;
   const uint32_t gcol = static_cast<uint32_t>(T.mat) * static_cast<uint32_t>(p.cols) + static_cast<uint32_t>(T.c0 + lc);
+  const uint32_t group0 = static_cast<uint32_t>((T.r0 >> 3) + rb * 4);
+  const uint32_t group[4] = {group0, group0 + 1, group0 + 2, group0 + 3};
   uint32_t w[kCols][4];
 #pragma unroll
-  for (int g = 0; g < 4; ++g) {
-    float y[kCols][8];
+  for (int h = 0; h < kCols; ++h) {
+    uint4 num[4];
+    if (kStoch) philox8x4(key, kRngCols, gcol + h, group, num);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      if constexpr (C::kHalf) {
-        const float2 f = mul_bf16x2_f32(raw[g * 8 + j], inv2);
-        y[0][j] = kDrop ? f.x * mul * inv[0] : f.x;
-        y[1][j] = kDrop ? f.y * mul * inv[1] : f.y;
-      } else {
-        y[0][j] = kDrop ? __uint_as_float(raw[g * 8 + j]) * mul * inv[0] : __uint_as_float(raw[g * 8 + j]) * inv[0];
+    for (int g = 0; g < 4; ++g) {
+      float y[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if constexpr (C::kHalf) {
+          const float2 f = mul_bf16x2_f32(raw[g * 8 + j], inv2);
+          y[j] = h ? f.y : f.x;
+          if (kDrop) y[j] = y[j] * mul * inv[h];
+        } else {
+          y[j] = kDrop ? __uint_as_float(raw[g * 8 + j]) * mul * inv[0] : __uint_as_float(raw[g * 8 + j]) * inv[0];
+        }
       }
-    }
-#pragma unroll
-    for (int h = 0; h < kCols; ++h) {
-      w[h][g] = kStoch ? pack8_stochastic(y[h], philox8(key, kRngCols, gcol + h,
-                                                        static_cast<uint32_t>((T.r0 >> 3) + rb * 4 + g)))
-                       : pack8_e2m1(y[h]);
+      w[h][g] = kStoch ? pack8_stochastic(y, num[g]) : pack8_e2m1(y);
       if (byte[h] == 255u) w[h][g] = 0u;
     }
   }

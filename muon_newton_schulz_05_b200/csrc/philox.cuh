@@ -43,4 +43,35 @@ __device__ __forceinline__ uint4 philox8(const RngKey& key, uint32_t domain, uin
   return make_uint4(c0, c1, c2, c3);
 }
 
+// Four calls at once, for groups g[0..3] of one row: the round keys are formed
+// once, and the four chains fill each other's latencies.
+__device__ __forceinline__ void philox8x4(const RngKey& key, uint32_t domain, uint32_t row,
+                                          const uint32_t (&g)[4], uint4 (&out)[4]) {
+  uint32_t c0[4], c1[4], c2[4], c3[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    c0[j] = g[j];
+    c1[j] = row;
+    c2[j] = key.n_lo;
+    c3[j] = key.n_hi | (domain << 30);
+  }
+  uint32_t k0 = key.k0, k1 = key.k1;
+#pragma unroll
+  for (int i = 0; i < 10; ++i) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint64_t p = static_cast<uint64_t>(0xD2511F53u) * c0[j];
+      const uint64_t q = static_cast<uint64_t>(0xCD9E8D57u) * c2[j];
+      c0[j] = static_cast<uint32_t>(q >> 32) ^ c1[j] ^ k0;
+      c1[j] = static_cast<uint32_t>(q);
+      c2[j] = static_cast<uint32_t>(p >> 32) ^ c3[j] ^ k1;
+      c3[j] = static_cast<uint32_t>(p);
+    }
+    k0 += 0x9E3779B9u;
+    k1 += 0xBB67AE85u;
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) out[j] = make_uint4(c0[j], c1[j], c2[j], c3[j]);
+}
+
 }  // namespace muon
