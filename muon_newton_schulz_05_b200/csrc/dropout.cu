@@ -41,9 +41,72 @@ __global__ void __launch_bounds__(256) dropout_kernel(const __grid_constant__ Dr
   }
 }
 
-// Any row length: a warp takes 32 groups, forms their numbers, and passes
-// them through shared memory so that neighbouring lanes handle neighbouring
-// elements.
+// Other row lengths, from 16 on: the buffers are contiguous, so a thread still
+// takes eight elements of the flat array with 16-byte accesses. They begin
+// anywhere in a row: their numbers are those of the group they begin in, which
+// this thread forms, and of the next one, which the next thread forms. Where a
+// row ends among the eight, the next thread's group is the next row's first.
+template <bool kBf16, bool kResidual>
+__global__ void __launch_bounds__(256) dropout_flat_kernel(const __grid_constant__ DropoutParams p, uint32_t n) {
+  __shared__ uint4 numbers[257];
+  const RngKey key = rng_key(p.rng, p.site);
+  const uint16_t* u = reinterpret_cast<const uint16_t*>(numbers);
+  const uint32_t step = gridDim.x * 2048u;
+  for (uint32_t base = blockIdx.x * 2048u; base < n; base += step) {
+    const uint32_t at = base + threadIdx.x * 8u;
+    const int row = fdiv(static_cast<int>(at), p.fd_cols);
+    const int col = static_cast<int>(at) - row * p.cols;
+    float x[8], r[8];
+    const bool whole = at + 8 <= n;
+    if (whole) {
+      load8t<kBf16>(p.x, at, x);
+      if (kResidual) load8t<kBf16>(p.residual, at, r);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        x[j] = at + j < n ? load1t<kBf16>(p.x, at + j) : 0.0f;
+        if (kResidual) r[j] = at + j < n ? load1t<kBf16>(p.residual, at + j) : 0.0f;
+      }
+    }
+    numbers[threadIdx.x] = philox8(key, kRngDropout, static_cast<uint32_t>(row), static_cast<uint32_t>(col >> 3));
+    if (threadIdx.x == 255) {   // the group of the first element behind this block's
+      const bool wraps = col + 8 >= p.cols;
+      numbers[256] = philox8(key, kRngDropout, static_cast<uint32_t>(wraps ? row + 1 : row),
+                             static_cast<uint32_t>((wraps ? col + 8 - p.cols : col + 8) >> 3));
+    }
+    __syncthreads();
+    const int left = p.cols - col;            // elements up to the row's end
+    const int first = col & 7;                // of the own group
+    uint4 tail = make_uint4(0u, 0u, 0u, 0u);  // the row's last group, where it is neither of the two
+    const bool extra = left <= 8 && first + left > 8;
+    if (extra)
+      tail = philox8(key, kRngDropout, static_cast<uint32_t>(row), static_cast<uint32_t>((col >> 3) + 1));
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      uint32_t k;
+      if (j >= left)
+        k = u[(threadIdx.x + 1) * 8 + j - left];
+      else if (extra && first + j >= 8)
+        k = half_of(tail, first + j - 8);
+      else
+        k = u[threadIdx.x * 8 + first + j];
+      x[j] = dropped(x[j], k, p.threshold, p.scale);
+      if (kResidual) x[j] += r[j];
+    }
+    if (whole) {
+      store8t<kBf16>(p.out, at, x);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (at + j < n) store1t<kBf16>(p.out, at + j, x[j]);
+    }
+    __syncthreads();
+  }
+}
+
+// Any row length and size, element by element: a warp takes 32 groups, forms
+// their numbers, and passes them through shared memory so that neighbouring
+// lanes handle neighbouring elements.
 template <bool kBf16, bool kResidual>
 __global__ void __launch_bounds__(256) dropout_ragged_kernel(const __grid_constant__ DropoutParams p) {
   __shared__ uint4 numbers[8][32];
@@ -81,10 +144,15 @@ template <bool kBf16, bool kResidual>
 static cudaError_t launch_typed(const DropoutParams& p, int sms, cudaStream_t s) {
   const uint32_t want = (p.total + 255) / 256, most = 32u * static_cast<uint32_t>(sms);
   const uint32_t grid = want < most ? want : most;
-  if (p.cols % 8 == 0)
+  const long long n = p.rows * p.cols;
+  if (p.cols % 8 == 0) {
     dropout_kernel<kBf16, kResidual><<<grid, 256, 0, s>>>(p);
-  else
+  } else if (p.cols >= 16 && n < (1LL << 31) - 4096) {   // 32-bit flat indices
+    const uint32_t blocks = static_cast<uint32_t>((n + 2047) / 2048);
+    dropout_flat_kernel<kBf16, kResidual><<<blocks < most ? blocks : most, 256, 0, s>>>(p, static_cast<uint32_t>(n));
+  } else {
     dropout_ragged_kernel<kBf16, kResidual><<<grid, 256, 0, s>>>(p);
+  }
   return cudaGetLastError();
 }
 

@@ -32,7 +32,7 @@ struct DropoutParams {
   long long rows;
   int cols;
   int groups;                   // ceil(cols / 8)
-  FastDiv fd_groups;
+  FastDiv fd_groups, fd_cols;
   uint32_t total;               // rows * groups (< 2^31)
   uint32_t threshold;           // dropped when the 16-bit number is below it
   float scale;                  // 2^16 / (2^16 - threshold)
@@ -61,7 +61,7 @@ struct DequantParams {
   int count, rows, cols;
   int blocks, tiles_r, tiles_c;
   int groups;                   // ceil(cols / 8)
-  FastDiv fd_groups, fd_rows;
+  FastDiv fd_groups, fd_rows, fd_cols;
   uint32_t total;               // count * rows * groups (< 2^31)
 };
 

@@ -204,6 +204,7 @@ muon_status muon_dropout(const void* x, const void* residual, void* out, int32_t
   d.cols = static_cast<int>(cols);
   d.groups = static_cast<int>(ceil_div(cols, 8));
   d.fd_groups = make_fastdiv(static_cast<uint32_t>(d.groups));
+  d.fd_cols = make_fastdiv(static_cast<uint32_t>(cols));
   d.total = static_cast<uint32_t>(rows * d.groups);
   return launch_dropout(d, dtype == MUON_BF16, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess
              ? MUON_OK
@@ -262,6 +263,7 @@ muon_status muon_mxfp4_dequantize(const muon_mxfp4* q, void* out, int32_t dtype,
   d.groups = static_cast<int>(groups);
   d.fd_groups = make_fastdiv(static_cast<uint32_t>(groups));
   d.fd_rows = make_fastdiv(static_cast<uint32_t>(q->rows));
+  d.fd_cols = make_fastdiv(static_cast<uint32_t>(q->cols));
   d.total = static_cast<uint32_t>(q->count * q->rows * groups);
   return launch_dequantize(d, dtype == MUON_BF16, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess
              ? MUON_OK

@@ -543,9 +543,14 @@ cudaError_t launch_quantize(const QuantParams& p, bool bf16, int sms, cudaStream
 }
 
 // ------------------------------------------------------------------ read-back
-__device__ __forceinline__ void decode8(uint32_t w, uint32_t byte, float (&v)[8]) {
-  // 2^(byte - 127); byte 0 is the subnormal 2^-127, byte 255 is NaN
-  const float scale = __uint_as_float(byte == 0u ? 0x00400000u : (byte == 255u ? 0x7FC00000u : byte << 23));
+// 2^(byte - 127); byte 0 is the subnormal 2^-127, byte 255 is NaN.
+__device__ __forceinline__ float scale_value(uint32_t byte) {
+  return __uint_as_float(byte == 0u ? 0x00400000u : (byte == 255u ? 0x7FC00000u : byte << 23));
+}
+
+// Eight codes; the first n of them have scale byte b0, the others b1.
+__device__ __forceinline__ void decode8(uint32_t w, uint32_t b0, uint32_t b1, int n, float (&v)[8]) {
+  const float scale0 = scale_value(b0), scale1 = scale_value(b1);
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     uint32_t h2;
@@ -553,10 +558,12 @@ __device__ __forceinline__ void decode8(uint32_t w, uint32_t byte, float (&v)[8]
         : "=r"(h2)
         : "h"(static_cast<uint16_t>((w >> (8 * j)) & 0xFFu)));
     const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h2));
-    v[2 * j] = f.x * scale;
-    v[2 * j + 1] = f.y * scale;
+    v[2 * j] = f.x * (2 * j < n ? scale0 : scale1);
+    v[2 * j + 1] = f.y * (2 * j + 1 < n ? scale0 : scale1);
   }
 }
+
+__device__ __forceinline__ void decode8(uint32_t w, uint32_t byte, float (&v)[8]) { decode8(w, byte, byte, 8, v); }
 
 __device__ __forceinline__ uint32_t scale_at(const DequantParams& p, int mat, int row, int block) {
   const long long t = (static_cast<long long>(mat) * p.tiles_r + (row >> 7)) * p.tiles_c + (block >> 2);
@@ -595,7 +602,47 @@ __global__ void __launch_bounds__(256) dequantize_kernel(const __grid_constant__
   }
 }
 
-// Any row length: a warp decodes 32 groups and passes them through shared
+// Other row lengths, from 8 on: out is contiguous, so a thread still stores
+// eight elements of the flat array at once. Their codes are a window of two
+// words of a row; where a row ends among the eight, the rest begins the next.
+template <bool kBf16>
+__global__ void __launch_bounds__(256) dequantize_flat_kernel(const __grid_constant__ DequantParams p, uint32_t n) {
+  const uint32_t at = (blockIdx.x * 256u + threadIdx.x) * 8u;
+  if (at >= n) return;
+  const int grow = fdiv(static_cast<int>(at), p.fd_cols);
+  const int col = static_cast<int>(at) - grow * p.cols;
+  auto window = [&](int gr, int c, float (&v)[8]) {   // the eight values from column c of a row on
+    const int mat = fdiv(gr, p.fd_rows), row = gr - mat * p.rows;
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(p.q + static_cast<long long>(gr) * p.blocks * 16) + (c >> 3);
+    const uint32_t lo = w[0], hi = (c >> 3) + 1 < p.blocks * 4 ? w[1] : 0u;
+    const int block = c >> 5, next = min(block + 1, p.blocks - 1);
+    const uint32_t s0 = scale_at(p, mat, row, block), s1 = scale_at(p, mat, row, next);
+    decode8(__funnelshift_r(lo, hi, 4 * (c & 7)), s0, s1, 32 - (c & 31), v);
+  };
+  float v[8];
+  window(grow, col, v);
+  const int left = p.cols - col;
+  if (left < 8 && at + left < n) {
+    float t[8];
+    window(grow + 1, 0, t);
+#pragma unroll
+    for (int j = 1; j < 8; ++j) {
+      // v[j] = t[j - left] for j >= left, without indexing registers
+#pragma unroll
+      for (int i = 0; i < 7; ++i)
+        if (j - left == i) v[j] = t[i];
+    }
+  }
+  if (at + 8 <= n) {
+    store8t<kBf16>(p.out, at, v);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (at + j < n) store1t<kBf16>(p.out, at + j, v[j]);
+  }
+}
+
+// Any row length and size, element by element: a warp decodes 32 groups and passes them through shared
 // memory, so that neighbouring lanes store neighbouring elements.
 template <bool kBf16>
 __global__ void __launch_bounds__(256) dequantize_ragged_kernel(const __grid_constant__ DequantParams p) {
@@ -636,6 +683,11 @@ cudaError_t launch_dequantize(const DequantParams& p, bool bf16, int sms, cudaSt
     const uint32_t blocks = static_cast<uint32_t>(p.count) * p.tiles_r * p.tiles_c;
     if (bf16) dequantize_kernel<true><<<blocks, 256, 0, s>>>(p);
     else dequantize_kernel<false><<<blocks, 256, 0, s>>>(p);
+  } else if (const long long n = static_cast<long long>(p.count) * p.rows * p.cols;
+             p.cols >= 8 && n < (1LL << 31) - 4096) {   // 32-bit flat indices
+    const uint32_t blocks = static_cast<uint32_t>((n + 2047) / 2048);
+    if (bf16) dequantize_flat_kernel<true><<<blocks, 256, 0, s>>>(p, static_cast<uint32_t>(n));
+    else dequantize_flat_kernel<false><<<blocks, 256, 0, s>>>(p, static_cast<uint32_t>(n));
   } else {
     if (bf16) dequantize_ragged_kernel<true><<<grid, 256, 0, s>>>(p);
     else dequantize_ragged_kernel<false><<<grid, 256, 0, s>>>(p);

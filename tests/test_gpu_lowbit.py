@@ -49,7 +49,8 @@ def _source(rows, cols, dtype, seed, spread=1.0):
 
 # -------------------------------------------------------------------- dropout
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-@pytest.mark.parametrize("shape", [(1, 1), (1, 7), (3, 8), (5, 64), (33, 71), (257, 1001), (512, 1024)])
+@pytest.mark.parametrize("shape", [(1, 1), (1, 7), (3, 8), (5, 64), (33, 71), (257, 1001), (512, 1024),
+                                   (700, 17), (301, 18), (129, 23), (90, 33), (1, 2050), (40, 2047), (700, 9)])
 @pytest.mark.parametrize("residual", [False, True])
 def test_dropout(mb, shape, dtype, residual):
     x, r = _source(*shape, dtype, 1), _source(*shape, dtype, 2)
@@ -126,7 +127,7 @@ def _check_stored(mb, q, x, numbers=None):
 
 
 SHAPES = [(1, 1, 1), (1, 1, 40), (1, 40, 1), (2, 33, 31), (1, 128, 128), (3, 129, 72), (1, 5, 300), (2, 260, 136),
-          (1, 131, 1023)]
+          (1, 131, 1023), (2, 300, 9), (1, 200, 17), (3, 70, 35)]
 
 
 @pytest.mark.parametrize("shape", SHAPES, ids=str)
