@@ -329,6 +329,9 @@ muon_status muon_mxfp4_matmul(const muon_mxfp4* a, const muon_mxfp4* b, const vo
   p.share_r = r->count == 1 ? 1 : 0;
   p.tiles_l = static_cast<int>(ceil_div(l->rows, kMxTile));
   p.tiles_r = static_cast<int>(ceil_div(r->rows, kMxTile));
+  p.sf_l = static_cast<const uint8_t*>(l->scales);
+  p.sf_r = static_cast<const uint8_t*>(r->scales);
+  p.sf_groups = static_cast<int>(ceil_div(s.k, kMxTile));
   p.k64 = static_cast<int>(ceil_div(s.k, 64));
   p.kstages = static_cast<int>(ceil_div(s.k, 256));
   p.split = pl.split;

@@ -17,7 +17,7 @@
 // first, and the next tile's MMAs start as soon as it has. Products with few tiles and a long K are split along K into fp32
 // partial tiles, which a second kernel adds in split order (deterministic).
 //
-// few-row kernel: for products with at most 128 rows on one side. The other
+// few-row kernel: for products with at most 64 rows on one side. The other
 // operand, usually the weights, takes the MMA's 128-row side and is streamed
 // once; the K range of a tile is split over the CTAs of a cluster, which add
 // their partial tiles through distributed shared memory in rank order.
@@ -542,8 +542,12 @@ __global__ void __launch_bounds__(256) mx_reduce_kernel(const __grid_constant__ 
 
 // -------------------------------------------------------------- few-row kernel
 // One tile of 128 left rows x NT right rows per cluster; CTA r of the cluster
-// takes K stages r * kc .. and the cluster adds the parts. 192 threads: warp 0
-// loads, warp 1 issues the MMAs, warps 2..5 are the epilogue.
+// takes K stages r * kc .. and sends its part to the CTAs that add it up, each
+// some of the right rows, by bulk copies between the CTAs' shared memories,
+// counted on the receiver's barrier. (Reading the parts out of the other CTAs'
+// memory took another cluster barrier; sending them value by value with
+// st.async took 0.13 us per right row.) 192 threads: warp 0 loads,
+// warp 1 issues the MMAs, warps 2..5 are the epilogue.
 constexpr int kFewThreads = 192;
 constexpr int kFewSplit = 8;       // most CTAs per cluster
 
@@ -569,19 +573,23 @@ __device__ __forceinline__ void store_quad(const MxGemmParams& p, long long at, 
 template <int NT>
 __host__ __device__ constexpr int few_stage_bytes() { return kCodeBytes + NT * kKBytes + 2 * kSfGroupBytes; }
 
+// Stages in shared memory at most; each has scale columns of its own in TMEM
+// (8 for the left operand, 8 for the right), so that the MMAs of one stage do
+// not wait for those of the stage before. With the accumulator: 128 columns.
 template <int NT>
-__host__ __device__ constexpr uint32_t few_tmem_columns() { return NT + 16 <= 32 ? 32 : NT + 16 <= 64 ? 64 : NT + 16 <= 128 ? 128 : 256; }
+__host__ __device__ constexpr int few_ring() { return NT == 16 ? 5 : 4; }
+
+constexpr uint32_t kFewColumns = 128;
 
 template <int NT, bool kBf16>
 __global__ void __launch_bounds__(kFewThreads) mx_gemm_few_kernel(const __grid_constant__ MxGemmParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  __shared__ uint64_t full[16], empty[16], done;
+  __shared__ uint64_t full[few_ring<NT>()], empty[few_ring<NT>()], sready[few_ring<NT>()], done, parts;
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_word;
   constexpr int kStage = few_stage_bytes<NT>();
-  constexpr uint32_t kCols = few_tmem_columns<NT>();
-  constexpr uint32_t kSf = NT;               // 8 columns for the left scales, 8 for the right
+  static_assert(NT + 16 * few_ring<NT>() <= kFewColumns, "accumulator and scales");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint64_t limit = p.wait_limit_ns;
   volatile int* abort_flag = &abort_word;
@@ -589,110 +597,132 @@ __global__ void __launch_bounds__(kFewThreads) mx_gemm_few_kernel(const __grid_c
   const int tile = static_cast<int>(blockIdx.x) / p.split;
   const int c = tile / p.tm, im = tile - c * p.tm;
   const int kb0 = split * p.kc, nkb = min(p.kc, p.kstages - kb0);
+  // split tiles: this CTA adds up the right rows x0 .. x0 + xn - 1
+  const int xs = (NT + p.split - 1) / p.split, x0 = split * xs, xn = max(0, min(xs, p.n - x0));
+  uint8_t* received = smem + max(p.ring * kStage, NT * kRows * 4);
 
+  auto load = [&](int kb, int stage) {
+    const int cl = p.share_l ? 0 : c, cr = p.share_r ? 0 : c;
+    uint8_t* st = smem + stage * kStage;
+    const int k = kb0 + kb;
+    const uint32_t sf = static_cast<uint32_t>(min(2, p.sf_groups - 2 * k)) * kMxTileBytes;
+    uint8_t* sl = st + kCodeBytes + NT * kKBytes;
+    mbar_arrive_expect_tx(&full[stage], kCodeBytes + NT * kKBytes + 2 * sf);
+    tma_load_3d(st, &p.rows_l, &full[stage], k * kKBytes, im * kRows, cl);
+    tma_load_3d(st + kCodeBytes, &p.rows_r, &full[stage], k * kKBytes, 0, cr);
+    // contiguous, so they need no tensor map (fetching one costs a cold call
+    // about half a microsecond)
+    bulk_load(sl, p.sf_l + (static_cast<long long>(cl * p.tiles_l + im) * p.sf_groups + 2 * k) * kMxTileBytes, sf,
+              &full[stage]);
+    bulk_load(sl + kSfGroupBytes, p.sf_r + (static_cast<long long>(cr) * p.tiles_r * p.sf_groups + 2 * k) * kMxTileBytes,
+              sf, &full[stage]);
+  };
+
+  if (threadIdx.x == 64) tma_prefetch_map(&p.rows_l);
+  if (threadIdx.x == 96) tma_prefetch_map(&p.rows_r);
   if (threadIdx.x == 0) {
-    tma_prefetch_map(&p.rows_l);
-    tma_prefetch_map(&p.rows_r);
-    tma_prefetch_map(&p.scales_l);
-    tma_prefetch_map(&p.scales_r);
     for (int s = 0; s < p.ring; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
+      mbar_init(&sready[s], 4);
     }
     mbar_init(&done, 1);
+    mbar_init(&parts, 1);
     abort_word = 0;
     fence_mbar_init();
+    if (p.split > 1) mbar_arrive_expect_tx(&parts, static_cast<uint32_t>(p.split * xn * kRows * 4));
+    // the first loads leave before the TMEM allocation and the barrier
+#pragma unroll 1
+    for (int kb = 0; kb < min(p.ring, nkb); ++kb) load(kb, kb);
   }
   if (warp == 1) {
-    tmem_alloc(&tmem_slot, kCols);
+    tmem_alloc(&tmem_slot, kFewColumns);
     tmem_relinquish();
   }
   tc_fence_before();
   __syncthreads();
+  if (p.split > 1) cluster_arrive();   // this CTA's barriers are initialised
   tc_fence_after();
   const uint32_t tmem_base = tmem_slot;
 
-  bool ok = true;
   if (warp == 0) {
     if (lane == 0) {
-      const int cl = p.share_l ? 0 : c, cr = p.share_r ? 0 : c;
-      int stage = 0;
+      int stage = 0, sent = min(p.ring, nkb);
       uint32_t phase = 0;
-      int sent = 0;
-      for (int kb = 0; kb < nkb; ++kb, ++sent) {
-        if (kb >= p.ring && !mbar_wait(&empty[stage], phase ^ 1u, abort_flag, p.status, limit)) break;
-        uint8_t* st = smem + stage * kStage;
-        const int k = kb0 + kb;
-        mbar_arrive_expect_tx(&full[stage], kStage);
-        tma_load_3d(st, &p.rows_l, &full[stage], k * kKBytes, im * kRows, cl);
-        tma_load_3d(st + kCodeBytes, &p.rows_r, &full[stage], k * kKBytes, 0, cr);
-        tma_load_2d(st + kCodeBytes + NT * kKBytes, &p.scales_l, &full[stage], k * 256, cl * p.tiles_l + im);
-        tma_load_2d(st + kCodeBytes + NT * kKBytes + kSfGroupBytes, &p.scales_r, &full[stage], k * 256,
-                    cr * p.tiles_r);
+      for (int kb = sent; kb < nkb; ++kb, ++sent) {
+        if (!mbar_wait(&empty[stage], phase, abort_flag, p.status, limit)) break;
+        load(kb, stage);
         if (++stage == p.ring) { stage = 0; phase ^= 1u; }
       }
-      // every load has landed before shared memory is reused or released
+      // every load has landed before shared memory is released
       for (int kb = sent > p.ring ? sent - p.ring : 0; kb < sent; ++kb)
         drain(&full[kb % p.ring], static_cast<uint32_t>(kb / p.ring) & 1u, limit);
     }
+    __syncwarp();
   } else if (warp == 1) {
     if (lane == 0) {
       int stage = 0;
       uint32_t phase = 0;
+      const uint64_t desc0 = smem_desc_sw128(smem_u32(smem), 16, 1024);
+      // kept short (no unrolling): a call's few stages run from a cold
+      // instruction cache
+#pragma unroll 1
       for (int kb = 0; kb < nkb; ++kb) {
-        if (!mbar_wait(&full[stage], phase, abort_flag, p.status, limit)) break;
-        if (kb > 0) {  // one scale buffer: the MMAs of the stage before are done
-          const int before = kb - 1;
-          if (!mbar_wait(&empty[before % p.ring], static_cast<uint32_t>(before / p.ring) & 1u, abort_flag,
-                         p.status, limit))
-            break;
-        }
+        if (!mbar_wait(&full[stage], phase, abort_flag, p.status, limit) ||
+            !mbar_wait(&sready[stage], phase, abort_flag, p.status, limit))
+          break;
         tc_fence_after();
-        const uint32_t a = smem_u32(smem + stage * kStage);
-        const uint32_t b = a + kCodeBytes, sa = b + NT * kKBytes, sb = sa + kSfGroupBytes;
-        const uint32_t sfa = tmem_base + kSf, sfb = sfa + 8;
-#pragma unroll
-        for (int g = 0; g < 2; ++g) {
-          tmem_copy_scales(sfa + 4 * g, smem_desc_scales(sa + g * kMxTileBytes));
-          tmem_copy_scales(sfb + 4 * g, smem_desc_scales(sb + g * kMxTileBytes));
-        }
+        const uint32_t sfa = tmem_base + NT + static_cast<uint32_t>(stage) * 16u, sfb = sfa + 8;
+        const uint64_t a = desc0 + static_cast<uint32_t>(stage * (kStage >> 4)), b = a + (kCodeBytes >> 4);
         const int steps = min(4, p.k64 - 4 * (kb0 + kb));
-#pragma unroll
-        for (int ks = 0; ks < 4; ++ks) {
-          if (ks < steps)
-            umma_mxf4(tmem_base, smem_desc_sw128(a + ks * 32, 16, 1024), smem_desc_sw128(b + ks * 32, 16, 1024),
-                      idesc_mxf4(kRows, NT, 2 * (ks & 1)), sfa + 4 * (ks >> 1), sfb + 4 * (ks >> 1),
-                      (kb > 0 || ks > 0) ? 1u : 0u);
-        }
+#pragma unroll 1
+        for (int ks = 0; ks < steps; ++ks)
+          umma_mxf4(tmem_base, a + 2 * ks, b + 2 * ks, idesc_mxf4(kRows, NT, 2 * (ks & 1)), sfa + 4 * (ks >> 1),
+                    sfb + 4 * (ks >> 1), (kb > 0 || ks > 0) ? 1u : 0u);
         umma_commit(&empty[stage]);
         if (++stage == p.ring) { stage = 0; phase ^= 1u; }
       }
       umma_commit(&done);
     }
     __syncwarp();
+  } else {
+    // scales to TMEM, as in the pair kernel (one lane quadrant per warp)
+    int stage = 0;
+    uint32_t phase = 0;
+#pragma unroll 1
+    for (int kb = 0; kb < nkb; ++kb) {
+      if (!__all_sync(0xffffffffu, mbar_wait(&full[stage], phase, abort_flag, p.status, limit))) break;
+      const uint4* sf = reinterpret_cast<const uint4*>(smem + stage * kStage + kCodeBytes + NT * kKBytes) + lane;
+      tc_fence_after();
+      tmem_st16(tmem_base + (static_cast<uint32_t>(32 * (warp & 3)) << 16) + NT + static_cast<uint32_t>(stage) * 16u,
+                sf[0], sf[32], sf[64], sf[96]);
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sready[stage]);
+      if (++stage == p.ring) { stage = 0; phase ^= 1u; }
+    }
+    __syncwarp();
   }
-  // every warp waits: the parts are exchanged through the loads' shared memory
-  ok = mbar_wait(&done, 0, abort_flag, p.status, limit);
+  bool ok = mbar_wait(&done, 0, abort_flag, p.status, limit);
   if (!ok) drain(&done, 0, limit);
   ok = __syncthreads_and(ok && *abort_flag == 0);
   tc_fence_after();
 
-  // element (left row i, right row x) of this CTA's part, as [x][i]
-  float* mine = reinterpret_cast<float*>(smem);
   const int q = warp & 3;
+  const uint32_t tlane = tmem_base + (static_cast<uint32_t>(32 * q) << 16);
   if (p.split == 1) {
     if (ok && warp >= 2) {
       const int l = im * kRows + 32 * q + lane;
 #pragma unroll 1
-      for (int x0 = 0; x0 < NT; x0 += 8) {
-        if (x0 >= p.n) break;
+      for (int x = 0; x < p.n; x += 8) {
         uint32_t r[8];
-        tmem_ld8(tmem_base + (static_cast<uint32_t>(32 * q) << 16) + x0, r);
+        tmem_ld8(tlane + x, r);
         tmem_ld_wait();
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          if (l < p.m && x0 + j < p.n) {
-            const long long at = c * p.stride_c + l * p.stride_l + (x0 + j) * p.stride_r;
+          if (l < p.m && x + j < p.n) {
+            const long long at = c * p.stride_c + l * p.stride_l + (x + j) * p.stride_r;
             float v = __uint_as_float(r[j]);
             if (p.add) v += load1t<kBf16>(p.add, at);
             store1t<kBf16>(p.out, at, v);
@@ -701,65 +731,75 @@ __global__ void __launch_bounds__(kFewThreads) mx_gemm_few_kernel(const __grid_c
       }
     }
   } else {
-    if (warp >= 2) {
+    // the part as [right row][128], in the ring's memory (its loads have been
+    // consumed)
+    float* mine = reinterpret_cast<float*>(smem);
+    if (ok && warp >= 2) {
 #pragma unroll 1
-      for (int x0 = 0; x0 < NT; x0 += 8) {
+      for (int x = 0; x < p.n; x += 8) {
         uint32_t r[8];
-        tmem_ld8(tmem_base + (static_cast<uint32_t>(32 * q) << 16) + x0, r);
+        tmem_ld8(tlane + x, r);
         tmem_ld_wait();
 #pragma unroll
-        for (int j = 0; j < 8; ++j) mine[(x0 + j) * kRows + 32 * q + lane] = __uint_as_float(r[j]);
+        for (int j = 0; j < 8; ++j) mine[(x + j) * kRows + 32 * q + lane] = __uint_as_float(r[j]);
       }
+      fence_proxy_async_smem();
     }
-    // a part that failed poisons the status word; nothing of the tile is stored then
-    __shared__ int cluster_ok;
-    if (threadIdx.x == 0) cluster_ok = ok ? 1 : 0;
     __syncthreads();
-    cluster_sync();
-    // CTA r of the cluster adds right rows r, r + split, ... : four left rows
-    // per thread, all parts loaded before the first is added
-    const uint32_t part0 = smem_u32(mine), ok0 = smem_u32(&cluster_ok);
-    uint32_t all_ok = 1;
+    cluster_wait();   // every CTA's `parts` is initialised
+    if (ok && threadIdx.x < static_cast<unsigned>(p.split)) {
+      // thread r sends CTA r the right rows it adds up
+      const int owner = static_cast<int>(threadIdx.x), n = max(0, min(xs, p.n - owner * xs));
+      if (n > 0)
+        bulk_copy_cluster(mapa_shared(smem_u32(received) + static_cast<uint32_t>(split * xs * kRows * 4), owner),
+                          mine + owner * xs * kRows, static_cast<uint32_t>(n * kRows * 4),
+                          mapa_shared(smem_u32(&parts), owner));
+    }
+    // four left rows of a right row per thread; the parts are added in rank
+    // order. A part that never came leaves the tile unwritten.
+    if (xn > 0) ok = mbar_wait_cluster(&parts, 0, abort_flag, p.status, limit) && ok;
+    __syncwarp();
+    cluster_arrive_relaxed();   // what this CTA was sent has arrived
+    if (xn > 0) {
+      const float4* part = reinterpret_cast<const float4*>(received);
+      if (ok) {
+#pragma unroll 1
+        for (int e = static_cast<int>(threadIdx.x); e < xn * (kRows / 4); e += kFewThreads) {
+          float4 v[kFewSplit];
 #pragma unroll
-    for (int s = 0; s < kFewSplit; ++s)
-      if (s < p.split) all_ok &= ld_shared_cluster_u32(mapa_shared(ok0, s));
-    if (all_ok) {
-      const int quads = (p.n - split + p.split - 1) / p.split * (kRows / 4);
-      for (int e = static_cast<int>(threadIdx.x); e < quads; e += kFewThreads) {
-        const int x = (e >> 5) * p.split + split, i = (e & 31) * 4;
-        float4 v[kFewSplit];
+          for (int s = 0; s < kFewSplit; ++s)
+            if (s < p.split) v[s] = part[s * xs * (kRows / 4) + e];
+          float y[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
 #pragma unroll
-        for (int s = 0; s < kFewSplit; ++s)
-          if (s < p.split) v[s] = ld_shared_cluster_f32x4(mapa_shared(part0 + (x * kRows + i) * 4, s));
-        float y[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
-#pragma unroll
-        for (int s = 1; s < kFewSplit; ++s) {
-          if (s < p.split) {
-            y[0] += v[s].x; y[1] += v[s].y; y[2] += v[s].z; y[3] += v[s].w;
+          for (int s = 1; s < kFewSplit; ++s) {
+            if (s < p.split) {
+              y[0] += v[s].x; y[1] += v[s].y; y[2] += v[s].z; y[3] += v[s].w;
+            }
           }
-        }
-        const int l = im * kRows + i;
-        const long long at = c * p.stride_c + l * p.stride_l + x * p.stride_r;
-        if (p.stride_l == 1 && (p.stride_r & 3) == 0) {   // four neighbours of one row of out
-          if (l < p.m) store_quad<kBf16>(p, at, y);
-        } else {
+          const int l = im * kRows + (e & 31) * 4;
+          const long long at = c * p.stride_c + l * p.stride_l + (x0 + (e >> 5)) * p.stride_r;
+          if (p.stride_l == 1 && (p.stride_r & 3) == 0) {   // four neighbours of one row of out
+            if (l < p.m) store_quad<kBf16>(p, at, y);
+          } else {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            if (l + j < p.m) {
-              if (p.add) y[j] += load1t<kBf16>(p.add, at + j * p.stride_l);
-              store1t<kBf16>(p.out, at + j * p.stride_l, y[j]);
+            for (int j = 0; j < 4; ++j) {
+              if (l + j < p.m) {
+                if (p.add) y[j] += load1t<kBf16>(p.add, at + j * p.stride_l);
+                store1t<kBf16>(p.out, at + j * p.stride_l, y[j]);
+              }
             }
           }
         }
       }
     }
-    cluster_sync();   // the others have read this CTA's part
+    __syncwarp();
+    cluster_wait();   // and so has what it sent: its memory may go
   }
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem_base, kCols);
+    tmem_dealloc(tmem_base, kFewColumns);
   }
 }
 
@@ -768,34 +808,41 @@ MxGemmPlan plan_mx_gemm(const MxGemmShape& s, int pairs, int sms) {
   MxGemmPlan pl{};
   const int kstages = static_cast<int>((s.k + 255) / 256);
   const int64_t small = s.m < s.n ? s.m : s.n, large = s.m < s.n ? s.n : s.m;
-  if (small <= kRows) {
+  // Few rows on one side. Up to 32 the few-row kernel is faster everywhere (16 x
+  // 2560 x 2560: 6 against 10 us, 16 x 50304 x 768: 10 against 13); up to 64
+  // where the other side has few tiles too, so that K can be split over many
+  // CTAs (64 x 2560 x 2560: 8 against 10 us, but 64 x 10240 x 2560: 21 against 11).
+  const int64_t tall = (large + kRows - 1) / kRows;
+  if (small <= 32 || (small <= 64 && s.count * tall <= sms / 4)) {
     pl.few = true;
     pl.swap = s.m <= s.n;  // the left operand of the kernel is the one with many rows
-    pl.nt = small <= 16 ? 16 : small <= 32 ? 32 : small <= 64 ? 64 : 128;
-    pl.tm = static_cast<int>((large + kRows - 1) / kRows);
+    pl.nt = small <= 16 ? 16 : small <= 32 ? 32 : 64;
+    pl.tm = static_cast<int>(tall);
     pl.tn = 1;
-    // split K over the CTAs of a cluster (a power of two) while that
-    // still adds CTAs the device has room for
-    pl.split = 1;
-    while (pl.split < kFewSplit && pl.split * 2 <= kstages && s.count * pl.tm * pl.split * 2 <= 2 * sms) pl.split *= 2;
-    pl.kc = (kstages + pl.split - 1) / pl.split;
-    while (pl.split > 1 && pl.kc * (pl.split - 1) >= kstages) {  // no empty part
-      pl.split /= 2;
-      pl.kc = (kstages + pl.split - 1) / pl.split;
-    }
-    const int cap = pl.nt <= 32 ? 5 : 4;
+    // as many K parts as one wave of CTAs holds; two fit an SM, with 64
+    // columns one
+    const int64_t slots = pl.nt == 64 ? sms : 2 * sms;
+    int64_t split = slots / (s.count * tall);
+    if (split > kFewSplit) split = kFewSplit;
+    if (split > kstages) split = kstages;
+    if (split < 1) split = 1;
+    pl.kc = static_cast<int>((kstages + split - 1) / split);
+    pl.split = (kstages + pl.kc - 1) / pl.kc;   // no empty part
+    const int cap = pl.nt == 16 ? few_ring<16>() : few_ring<32>();
     pl.ring = pl.kc < cap ? pl.kc : cap;
     return pl;
   }
   pl.tm = static_cast<int>((s.m + kPTile - 1) / kPTile);
   pl.tn = static_cast<int>((s.n + kPTile - 1) / kPTile);
   const int64_t tiles = s.count * pl.tm * pl.tn;
+  // Few tiles and a long K: split it. A stage takes a pair about 0.44 us, and
+  // the partial tiles with the kernel that adds them 5.5 us, so at least 14
+  // stages have to be saved (768 x 768, 9 tiles: K 4096 13.0 us unsplit
+  // against 13.3-14.9, K 8192 20.0 against 14.0).
   pl.split = 1;
   if (tiles * 2 <= pairs) {
-    int64_t sp = pairs / tiles;
-    if (sp > kstages / 4) sp = kstages / 4;  // at least four stages each
-    if (sp > 16) sp = 16;
-    if (sp > 1) pl.split = static_cast<int>(sp);
+    const int64_t sp = pairs / tiles < 16 ? pairs / tiles : 16;
+    if (kstages - (kstages + sp - 1) / sp >= 14) pl.split = static_cast<int>(sp);
   }
   pl.kc = (kstages + pl.split - 1) / pl.split;
   pl.split = (kstages + pl.kc - 1) / pl.kc;
@@ -816,26 +863,24 @@ static const void* few_kernel_nt(bool bf16) {
 }
 
 static const void* few_kernel(int nt, bool bf16) {
-  return nt == 16 ? few_kernel_nt<16>(bf16)
-                  : nt == 32 ? few_kernel_nt<32>(bf16) : nt == 64 ? few_kernel_nt<64>(bf16) : few_kernel_nt<128>(bf16);
+  return nt == 16 ? few_kernel_nt<16>(bf16) : nt == 32 ? few_kernel_nt<32>(bf16) : few_kernel_nt<64>(bf16);
 }
 
-// Shared memory of the few-row kernel: the ring, which later holds the part.
+// Shared memory of the few-row kernel: the ring, which later holds the CTA's
+// part, and the parts received.
 static int few_smem(const MxGemmPlan& pl) {
-  const int stage = kCodeBytes + pl.nt * kKBytes + 2 * kSfGroupBytes;
-  int bytes = pl.ring * stage;
-  const int part = pl.split > 1 ? pl.nt * kRows * 4 : 0;
-  if (part > bytes) bytes = part;
-  return bytes + 1024;
+  const int ring = pl.ring * (kCodeBytes + pl.nt * kKBytes + 2 * kSfGroupBytes), part = pl.nt * kRows * 4;
+  const int received = (pl.nt + pl.split - 1) / pl.split * pl.split * kRows * 4;
+  return (pl.split > 1 ? (ring > part ? ring : part) + received : ring) + 1024;
 }
 
 cudaError_t mx_gemm_prepare(int* max_pairs) {
   cudaError_t e = cudaSuccess;
   for (int i = 0; i < 3 && e == cudaSuccess; ++i)
     e = cudaFuncSetAttribute(pair_kernel(i & 1, i & 2), cudaFuncAttributeMaxDynamicSharedMemorySize, kPSmemBytes);
-  for (int nt = 16; nt <= 128; nt *= 2)
+  for (int nt = 16; nt <= 64; nt *= 2)
     for (int b = 0; b < 2 && e == cudaSuccess; ++b)
-      e = cudaFuncSetAttribute(few_kernel(nt, b), cudaFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
+      e = cudaFuncSetAttribute(few_kernel(nt, b), cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024);
   if (e != cudaSuccess) return e;
   int dev = 0, sms = 0;
   if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;

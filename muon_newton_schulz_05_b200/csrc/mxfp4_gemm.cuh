@@ -10,6 +10,8 @@ struct MxGemmParams {
   CUtensorMap scales_l, scales_r;  // scale tiles: uint32 [count * tiles][ceil(blocks / 4) * 128]
   CUtensorMap result;              // pair kernel: out [count][m][n], boxes of 32 x 32 (if tma_out)
   int tma_out;
+  const uint8_t *sf_l, *sf_r;      // the scale tiles themselves (few-row kernel)
+  int sf_groups;                   // tiles per tile row
   const void* add;
   void* out;
   float* part;                     // split products: fp32 partial tiles in the workspace

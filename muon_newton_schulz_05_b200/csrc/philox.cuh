@@ -43,15 +43,16 @@ __device__ __forceinline__ uint4 philox8(const RngKey& key, uint32_t domain, uin
   return make_uint4(c0, c1, c2, c3);
 }
 
-// Four calls at once, for groups g[0..3] of one row: the round keys are formed
-// once, and the four chains fill each other's latencies.
-__device__ __forceinline__ void philox8x4(const RngKey& key, uint32_t domain, uint32_t row,
-                                          const uint32_t (&g)[4], uint4 (&out)[4]) {
-  uint32_t c0[4], c1[4], c2[4], c3[4];
+// N calls at once: the round keys are formed once, and the chains fill each
+// other's latencies.
+template <int N>
+__device__ __forceinline__ void philox8n(const RngKey& key, uint32_t domain, const uint32_t (&row)[N],
+                                         const uint32_t (&g)[N], uint4 (&out)[N]) {
+  uint32_t c0[N], c1[N], c2[N], c3[N];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
+  for (int j = 0; j < N; ++j) {
     c0[j] = g[j];
-    c1[j] = row;
+    c1[j] = row[j];
     c2[j] = key.n_lo;
     c3[j] = key.n_hi | (domain << 30);
   }
@@ -59,7 +60,7 @@ __device__ __forceinline__ void philox8x4(const RngKey& key, uint32_t domain, ui
 #pragma unroll
   for (int i = 0; i < 10; ++i) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < N; ++j) {
       const uint64_t p = static_cast<uint64_t>(0xD2511F53u) * c0[j];
       const uint64_t q = static_cast<uint64_t>(0xCD9E8D57u) * c2[j];
       c0[j] = static_cast<uint32_t>(q >> 32) ^ c1[j] ^ k0;
@@ -71,7 +72,14 @@ __device__ __forceinline__ void philox8x4(const RngKey& key, uint32_t domain, ui
     k1 += 0xBB67AE85u;
   }
 #pragma unroll
-  for (int j = 0; j < 4; ++j) out[j] = make_uint4(c0[j], c1[j], c2[j], c3[j]);
+  for (int j = 0; j < N; ++j) out[j] = make_uint4(c0[j], c1[j], c2[j], c3[j]);
+}
+
+// Four calls for groups g[0..3] of one row.
+__device__ __forceinline__ void philox8x4(const RngKey& key, uint32_t domain, uint32_t row,
+                                          const uint32_t (&g)[4], uint4 (&out)[4]) {
+  const uint32_t rows[4] = {row, row, row, row};
+  philox8n<4>(key, domain, rows, g, out);
 }
 
 }  // namespace muon
