@@ -307,13 +307,15 @@ class Mxfp4:
     """Matrices (count, rows, cols) in microscaled 4-bit floating point, blocks
     of 32 along cols. data: the codes, scales: one byte per block in tiles of
     128 rows x 4 blocks (both uint8; the header describes the layout)."""
-    __slots__ = ("data", "scales", "_shape", "_bytes")
+    __slots__ = ("data", "scales", "_shape", "_bytes", "_c", "_ref")
 
     def __init__(self, data, scales, shape):
         _need_torch()
         self.data, self.scales = data, scales
         self._shape = _shape3(shape)
         self._bytes = (int(_lib.muon_mxfp4_data_size(*self._shape)), int(_lib.muon_mxfp4_scales_size(*self._shape)))
+        self._c = CMxfp4(*self._shape, None, None)   # the pointers are set at each call
+        self._ref = ctypes.byref(self._c)
 
     @property
     def shape(self) -> Tuple[int, int, int]:
@@ -345,15 +347,17 @@ def alloc_mxfp4(shape, device="cuda") -> Mxfp4:
 
 
 def _cmx(q: Optional[Mxfp4], what: str):
+    """The C view of q, which its tensors must still fit."""
     if q is None:
         return None
-    n, m = q._bytes
-    d, s = q.data, q.scales
+    d, s, c = q.data, q.scales, q._c
     if d.dtype is not _torch.uint8 or s.dtype is not _torch.uint8:
         raise ValueError(f"{what}: data and scales must be uint8")
-    if n and (d.numel() != n or s.numel() != m):
-        raise ValueError(f"{what}: storage of {d.numel()} + {s.numel()} bytes for {n} + {m}")
-    return CMxfp4(*q._shape, _ptr(d), _ptr(s))
+    n = q._bytes[0]
+    if n and (d.numel() != n or s.numel() != q._bytes[1]):
+        raise ValueError(f"{what}: storage of {d.numel()} + {s.numel()} bytes for {n} + {q._bytes[1]}")
+    c.data, c.scales = _ptr(d), _ptr(s)
+    return q._ref
 
 
 def _launch(stream, fn, what, x, others, *args) -> None:
@@ -366,11 +370,11 @@ def _launch(stream, fn, what, x, others, *args) -> None:
             raise ValueError("the tensors of a call must be on one CUDA device")
     if dev < 0:
         raise ValueError("the tensors of a call must be on one CUDA device")
-    if dev != _torch.cuda.current_device():
+    if dev == _torch._C._cuda_getDevice():
+        code = fn(*args, _torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream_handle(stream))
+    else:
         with _torch.cuda.device(dev):
             code = fn(*args, _stream_handle(stream))
-    else:
-        code = fn(*args, _torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream_handle(stream))
     if code != 0:
         raise MuonError(code, what)
 
@@ -437,7 +441,8 @@ def mxfp4_dequantize(q: Mxfp4, out, stream=None) -> None:
     """out ([count, rows, cols] or [rows, cols], bf16 or fp32) = the values of
     q, exactly (2^128 and above become infinity)."""
     cq = _cmx(q, "q")
-    if _shape3(out.shape) != q._shape:
+    shape = tuple(out.shape)
+    if shape != q._shape and (q._shape[0] != 1 or shape != q._shape[1:]):
         raise ValueError("out must have q's shape")
     _launch(stream, _lib.muon_mxfp4_dequantize, "mxfp4_dequantize", out, (q.data, q.scales), cq, _ptr(out),
             _dtype_code(out))
@@ -468,10 +473,10 @@ def mxfp4_matmul(a: Mxfp4, b: Mxfp4, out, workspace, add=None, stream=None) -> N
     reports a device-side wait that ran out."""
     ca, cb = _cmx(a, "a"), _cmx(b, "b")
     (na, m, _), (nb, n, _) = a._shape, b._shape
-    shape = out.shape
-    if _shape3(shape) != (na if na > nb else nb, m, n):
+    shape, count = tuple(out.shape), na if na > nb else nb
+    if shape != (count, m, n) and (count != 1 or shape != (m, n)):
         raise ValueError("out must be [count, a's rows, b's rows]")
-    if add is not None and (add.shape != shape or add.dtype != out.dtype):
+    if add is not None and (add.shape != out.shape or add.dtype != out.dtype):
         raise ValueError("add must have out's shape and dtype")
     _launch(stream, _lib.muon_mxfp4_matmul, "mxfp4_matmul", out,
             (a.data, a.scales, b.data, b.scales, workspace, add), ca, cb, _ptr(add), _ptr(out), _dtype_code(out),

@@ -641,7 +641,7 @@ __global__ void __launch_bounds__(kFewThreads) mx_gemm_few_kernel(const __grid_c
   }
   tc_fence_before();
   __syncthreads();
-  if (p.split > 1) cluster_arrive();   // this CTA's barriers are initialised
+  if (p.split > 1) cluster_arrive_relaxed();   // this CTA's barriers are initialised (and fenced)
   tc_fence_after();
   const uint32_t tmem_base = tmem_slot;
 

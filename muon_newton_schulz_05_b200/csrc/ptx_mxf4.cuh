@@ -127,12 +127,8 @@ __device__ __forceinline__ void bulk_copy_cluster(uint32_t dst, const void* src,
       : "memory");
 }
 
-// The two halves of a cluster barrier (every thread of the cluster's CTAs);
-// the relaxed arrival orders no memory accesses.
-__device__ __forceinline__ void cluster_arrive() {
-  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-}
-
+// The two halves of a cluster barrier (every thread of the cluster's CTAs).
+// The arrival orders nothing but what a fence before it did.
 __device__ __forceinline__ void cluster_arrive_relaxed() {
   asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
 }
