@@ -334,6 +334,15 @@ def _shape3(shape) -> Tuple[int, int, int]:
     return (int(s[0]), int(s[1]), int(s[2]))
 
 
+def mxfp4_storage(shape) -> Tuple[int, int]:
+    """Bytes of the codes and of the scales of matrices of this shape."""
+    c, r, k = _shape3(shape)
+    n = int(_lib.muon_mxfp4_data_size(c, r, k))
+    if n == 0:
+        raise MuonError(2, "mxfp4_storage")
+    return n, int(_lib.muon_mxfp4_scales_size(c, r, k))
+
+
 def alloc_mxfp4(shape, device="cuda") -> Mxfp4:
     """Storage for matrices (count, rows, cols) or (rows, cols) in 4 bits."""
     import torch
@@ -513,7 +522,7 @@ def loaded_library_path() -> str:
 __all__: List[str] = ["Bank", "Hparams", "MuonError", "workspace_size", "alloc_workspace",
                       "muon_step", "anvil_step", "orthogonalize", "ema_update", "readout_blend",
                       "checkpoint_average_betas",
-                      "Mxfp4", "alloc_mxfp4", "dropout", "mxfp4_quantize", "mxfp4_readout",
+                      "Mxfp4", "alloc_mxfp4", "mxfp4_storage", "dropout", "mxfp4_quantize", "mxfp4_readout",
                       "mxfp4_dequantize", "mxfp4_matmul", "matmul_workspace_size",
                       "alloc_matmul_workspace", "CMxfp4",
                       "device_status", "set_debug", "set_ns_events", "status_string", "abi_version",

@@ -177,3 +177,30 @@ def test_binding_refusals():
 
 def test_struct_layout():
     assert ctypes.sizeof(mb.CMxfp4) == 40 and mb.CMxfp4.data.offset == 24
+
+
+def test_linear_layer_refusals():
+    from muon_newton_schulz_05_b200.fourbit import Mxfp4Linear
+    lin = Mxfp4Linear((2, 24, 40), tokens=7, p=0.1, device="cpu")
+    assert lin.w.shape == (2, 24, 40) and lin.w_t.shape == (2, 40, 24) and lin.dy_t.shape == (2, 24, 7)
+    x, y, w = torch.zeros(2, 7, 40), torch.zeros(2, 7, 24), torch.zeros(2, 24, 40)
+    cases = [
+        lambda: Mxfp4Linear((2, 24, 40), tokens=0, device="cpu"),
+        lambda: lin.refresh(torch.zeros(24, 40)),
+        lambda: lin.forward(x[:, :6], y),
+        lambda: lin.forward(x, y[:1]),
+        lambda: lin.infer(torch.zeros(2, 8, 40), torch.zeros(2, 8, 24)),
+        lambda: lin.infer(torch.zeros(2, 0, 40), torch.zeros(2, 0, 24)),
+        lambda: lin.backward(y, w),                                          # rng missing
+        lambda: lin.backward(x, w, rng=torch.zeros(2, dtype=torch.int64)),
+        lambda: lin.backward(y, w, dx=y, rng=torch.zeros(2, dtype=torch.int64)),
+    ]
+    for f in cases:
+        with pytest.raises(ValueError):
+            f()
+    with pytest.raises(mb.MuonError):
+        Mxfp4Linear((0, 24, 40), tokens=7, device="cpu")
+    # the forward workspace serves fewer tokens too: 256 rows of 80 tiles' worth are split along cols
+    lin = Mxfp4Linear((1, 256, 16384), tokens=20480, device="cpu")
+    for tokens in (1, 64, 65, 256, 257, 1000, 20480):
+        assert lin.ws_y.numel() >= mb.matmul_workspace_size((1, tokens, 16384), lin.w.shape)
