@@ -165,14 +165,25 @@ __device__ __forceinline__ void store_chunk(const MxGemmParams& p, uint8_t* buf,
           *reinterpret_cast<float4*>(static_cast<float*>(p.out) + at + 4LL * i * p.n) = v[i];
       }
     }
-  } else if (col + lane < p.n) {
+  } else if (col + lane < p.n) {   // one column per lane; the whole chunk is read before the first store
     const int rows = min(32, p.m - row);
     const long long at = base + static_cast<long long>(row) * p.n + col + lane;
-#pragma unroll 8
-    for (int rr = 0; rr < rows; ++rr) {
-      float v = *reinterpret_cast<const float*>(buf + rr * 128 + (((lane >> 2) ^ (rr & 7)) << 4) + (lane & 3) * 4);
-      if (p.add) v += load1t<kBf16>(p.add, at + static_cast<long long>(rr) * p.n);
-      store1t<kBf16>(p.out, at + static_cast<long long>(rr) * p.n, v);
+    float v[32];
+#pragma unroll
+    for (int rr = 0; rr < 32; ++rr)
+      v[rr] = *reinterpret_cast<const float*>(buf + rr * 128 + (((lane >> 2) ^ (rr & 7)) << 4) + (lane & 3) * 4);
+    if (p.add) {
+#pragma unroll
+      for (int rr = 0; rr < 32; ++rr)
+        if (rr < rows) v[rr] += load1t<kBf16>(p.add, at + static_cast<long long>(rr) * p.n);
+    }
+    if (rows == 32) {
+#pragma unroll
+      for (int rr = 0; rr < 32; ++rr) store1t<kBf16>(p.out, at + static_cast<long long>(rr) * p.n, v[rr]);
+    } else {
+#pragma unroll
+      for (int rr = 0; rr < 32; ++rr)
+        if (rr < rows) store1t<kBf16>(p.out, at + static_cast<long long>(rr) * p.n, v[rr]);
     }
   }
 }
@@ -469,6 +480,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
     __syncwarp();
   }
 
+  // let the kernel that adds the parts be launched (it waits for this grid)
+  if (kSplit) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   tc_fence_before();
   __syncthreads();
   cluster_sync();
@@ -486,6 +499,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
 template <bool kBf16>
 __global__ void __launch_bounds__(256) mx_reduce_kernel(const __grid_constant__ MxGemmParams p) {
   __shared__ float turn[32][33];
+  // launched while the pair kernel still runs: its partial tiles are complete
+  // once this returns
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   if (*reinterpret_cast<const volatile int*>(p.status) != 0) return;
   const int chunk = static_cast<int>(blockIdx.x & 63u), tile = static_cast<int>(blockIdx.x >> 6);
   const MxTile T = mx_tile(p, tile * p.split);
@@ -915,12 +931,16 @@ cudaError_t launch_mx_gemm(const MxGemmParams& p, const MxGemmPlan& plan, bool b
   cfg.dynamicSmemBytes = kPSmemBytes;
   cudaError_t e = cudaLaunchKernelExC(&cfg, pair_kernel(bf16, plan.split > 1), args);
   if (e != cudaSuccess || plan.split == 1) return e;
-  const unsigned blocks = static_cast<unsigned>(tiles) * 64u;
-  if (bf16)
-    mx_reduce_kernel<true><<<blocks, 256, 0, s>>>(p);
-  else
-    mx_reduce_kernel<false><<<blocks, 256, 0, s>>>(p);
-  return cudaGetLastError();
+  cfg.gridDim = dim3(static_cast<unsigned>(tiles) * 64u, 1, 1);
+  cfg.blockDim = dim3(256, 1, 1);
+  cfg.dynamicSmemBytes = 0;
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelExC(&cfg,
+                             bf16 ? reinterpret_cast<const void*>(&mx_reduce_kernel<true>)
+                                  : reinterpret_cast<const void*>(&mx_reduce_kernel<false>),
+                             args);
 }
 
 }  // namespace muon

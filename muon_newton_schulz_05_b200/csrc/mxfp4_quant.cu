@@ -607,38 +607,61 @@ __global__ void __launch_bounds__(256) dequantize_kernel(const __grid_constant__
 // words of a row; where a row ends among the eight, the rest begins the next.
 template <bool kBf16>
 __global__ void __launch_bounds__(256) dequantize_flat_kernel(const __grid_constant__ DequantParams p, uint32_t n) {
-  const uint32_t at = (blockIdx.x * 256u + threadIdx.x) * 8u;
-  if (at >= n) return;
-  const int grow = fdiv(static_cast<int>(at), p.fd_cols);
-  const int col = static_cast<int>(at) - grow * p.cols;
-  auto window = [&](int gr, int c, float (&v)[8]) {   // the eight values from column c of a row on
+  constexpr int kEach = 2;   // groups per thread, all loads first
+  struct Window {            // eight codes of a row from some column on, and their scales
+    uint32_t lo, hi, s0, s1;
+    int col;
+  };
+  auto fetch = [&](int gr, int c) {
     const int mat = fdiv(gr, p.fd_rows), row = gr - mat * p.rows;
     const uint32_t* w = reinterpret_cast<const uint32_t*>(p.q + static_cast<long long>(gr) * p.blocks * 16) + (c >> 3);
-    const uint32_t lo = w[0], hi = (c >> 3) + 1 < p.blocks * 4 ? w[1] : 0u;
-    const int block = c >> 5, next = min(block + 1, p.blocks - 1);
-    const uint32_t s0 = scale_at(p, mat, row, block), s1 = scale_at(p, mat, row, next);
-    decode8(__funnelshift_r(lo, hi, 4 * (c & 7)), s0, s1, 32 - (c & 31), v);
+    Window x;
+    x.lo = w[0];
+    x.hi = (c >> 3) + 1 < p.blocks * 4 ? w[1] : 0u;
+    x.s0 = scale_at(p, mat, row, c >> 5);
+    x.s1 = scale_at(p, mat, row, min((c >> 5) + 1, p.blocks - 1));
+    x.col = c;
+    return x;
   };
-  float v[8];
-  window(grow, col, v);
-  const int left = p.cols - col;
-  if (left < 8 && at + left < n) {
-    float t[8];
-    window(grow + 1, 0, t);
+  auto decode = [&](const Window& x, float (&v)[8]) {
+    decode8(__funnelshift_r(x.lo, x.hi, 4 * (x.col & 7)), x.s0, x.s1, 32 - (x.col & 31), v);
+  };
+  const uint32_t at0 = blockIdx.x * (2048u * kEach) + threadIdx.x * 8u;
+  Window own[kEach];
+  int row[kEach];
 #pragma unroll
-    for (int j = 1; j < 8; ++j) {
-      // v[j] = t[j - left] for j >= left, without indexing registers
-#pragma unroll
-      for (int i = 0; i < 7; ++i)
-        if (j - left == i) v[j] = t[i];
+  for (int e = 0; e < kEach; ++e) {
+    const uint32_t at = at0 + 2048u * e;
+    if (at < n) {
+      row[e] = fdiv(static_cast<int>(at), p.fd_cols);
+      own[e] = fetch(row[e], static_cast<int>(at) - row[e] * p.cols);
     }
   }
-  if (at + 8 <= n) {
-    store8t<kBf16>(p.out, at, v);
-  } else {
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (at + j < n) store1t<kBf16>(p.out, at + j, v[j]);
+  for (int e = 0; e < kEach; ++e) {
+    const uint32_t at = at0 + 2048u * e;
+    if (at >= n) continue;
+    float v[8];
+    decode(own[e], v);
+    const int left = p.cols - own[e].col;
+    if (left < 8 && at + left < n) {
+      float t[8];
+      decode(fetch(row[e] + 1, 0), t);
+#pragma unroll
+      for (int j = 1; j < 8; ++j) {
+        // v[j] = t[j - left] for j >= left, without indexing registers
+#pragma unroll
+        for (int i = 0; i < 7; ++i)
+          if (j - left == i) v[j] = t[i];
+      }
+    }
+    if (at + 8 <= n) {
+      store8t<kBf16>(p.out, at, v);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (at + j < n) store1t<kBf16>(p.out, at + j, v[j]);
+    }
   }
 }
 
@@ -685,7 +708,7 @@ cudaError_t launch_dequantize(const DequantParams& p, bool bf16, int sms, cudaSt
     else dequantize_kernel<false><<<blocks, 256, 0, s>>>(p);
   } else if (const long long n = static_cast<long long>(p.count) * p.rows * p.cols;
              p.cols >= 8 && n < (1LL << 31) - 4096) {   // 32-bit flat indices
-    const uint32_t blocks = static_cast<uint32_t>((n + 2047) / 2048);
+    const uint32_t blocks = static_cast<uint32_t>((n + 4095) / 4096);
     if (bf16) dequantize_flat_kernel<true><<<blocks, 256, 0, s>>>(p, static_cast<uint32_t>(n));
     else dequantize_flat_kernel<false><<<blocks, 256, 0, s>>>(p, static_cast<uint32_t>(n));
   } else {
