@@ -340,6 +340,13 @@ muon_status muon_mxfp4_matmul(const muon_mxfp4* a, const muon_mxfp4* b, const vo
   p.tm = pl.tm;
   p.tn = pl.tn;
   p.group = 8;
+  if (!pl.few) {
+    p.fd_split = make_fastdiv(static_cast<uint32_t>(pl.split));
+    p.fd_mat = make_fastdiv(static_cast<uint32_t>(pl.tm) * static_cast<uint32_t>(pl.tn));
+    p.fd_band = make_fastdiv(static_cast<uint32_t>(p.group) * static_cast<uint32_t>(pl.tn));
+    p.fd_group = make_fastdiv(static_cast<uint32_t>(p.group));
+    p.fd_rest = make_fastdiv(static_cast<uint32_t>(pl.tm % p.group));
+  }
   p.stride_l = pl.swap ? 1 : s.n;
   p.stride_r = pl.swap ? s.n : 1;
   p.stride_c = s.m * s.n;

@@ -73,17 +73,16 @@ struct MxTile {
 // CTAs at work at one time share operand rows in L2.
 __device__ __forceinline__ MxTile mx_tile(const MxGemmParams& p, int t) {
   MxTile x;
-  const int per_mat = p.tm * p.tn;
-  x.split = t % p.split;
-  t /= p.split;
-  x.c = t / per_mat;
-  t -= x.c * per_mat;
-  const int band = t / (p.group * p.tn);
+  const int u = fdiv(t, p.fd_split);
+  x.split = t - u * p.split;
+  x.c = fdiv(u, p.fd_mat);
+  t = u - x.c * (p.tm * p.tn);
+  const int band = fdiv(t, p.fd_band);
   const int first = band * p.group;
-  const int height = min(p.group, p.tm - first);
   t -= first * p.tn;
-  x.in = t / height;
-  x.im = first + t - x.in * height;
+  const bool whole = first + p.group <= p.tm;
+  x.in = fdiv(t, whole ? p.fd_group : p.fd_rest);
+  x.im = first + t - x.in * (whole ? p.group : p.tm - first);
   x.kb0 = x.split * p.kc;
   x.nkb = min(p.kc, p.kstages - x.kb0);
   return x;
@@ -242,7 +241,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
-  cluster_sync();
+  // the other CTA's barriers are initialised before any remote signal (thread
+  // 0 has fenced its own, so the arrival need not order anything)
+  cluster_arrive_relaxed();
+  cluster_wait();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
 
@@ -419,7 +421,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
     const uint32_t tnext_leader = mapa_shared(smem_u32(tnext), 0);
     const bool vec = (p.n % 4) == 0;
     uint8_t* buf = chunks + (warp - 2) * kPChunkBytes;
-    uint32_t acc = 0, phase = 0;
+    uint32_t acc = 0, phase = 0, chunk = 0;   // chunk: counts this warp's stores (its half buffers take turns)
     bool ok = true;
     for (int t = pair; ok && t < ntiles; t += npairs) {
       const MxTile T = mx_tile(p, t);
@@ -449,7 +451,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
             dst[g * 32 + lane] = make_float4(__uint_as_float(r[4 * g]), __uint_as_float(r[4 * g + 1]),
                                              __uint_as_float(r[4 * g + 2]), __uint_as_float(r[4 * g + 3]));
         } else if (p.tma_out) {
-          store_chunk_tma<kBf16>(p, buf, static_cast<uint32_t>(j), lane, r, T.c, row, col + j * 32);
+          store_chunk_tma<kBf16>(p, buf, chunk++, lane, r, T.c, row, col + j * 32);
         } else {
           store_chunk<kBf16>(p, buf, lane, r, T.c * p.stride_c, row, col + j * 32, vec);
         }
@@ -484,7 +486,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
   if (kSplit) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   tc_fence_before();
   __syncthreads();
-  cluster_sync();
+  cluster_arrive_relaxed();   // no MMA of the pair and no remote signal is still in flight
+  cluster_wait();
   if (warp == 1) {
     __syncwarp();
     tc_fence_after();

@@ -24,7 +24,8 @@ struct MxGemmParams {
   int split, kc;                   // K splits, stages per split
   int ring;                        // few-row kernel: pipeline stages in shared memory
   int tm, tn;                      // output tiles
-  int group;                       // row tiles per column sweep
+  int group;                       // row tiles per column sweep (a band)
+  FastDiv fd_split, fd_mat, fd_band, fd_group, fd_rest;  // by split, tm * tn, group * tn, group, the last band's rows
   long long stride_l, stride_r, stride_c;  // of out, per left row, right row and matrix
   int* status;
   unsigned long long wait_limit_ns;
