@@ -313,10 +313,9 @@ muon_status muon_mxfp4_matmul(const muon_mxfp4* a, const muon_mxfp4* b, const vo
                              static_cast<cuuint64_t>(s.count)};
     const cuuint64_t st2[2] = {static_cast<cuuint64_t>(s.n * dtype_size(out_dtype)),
                                static_cast<cuuint64_t>(s.m * s.n * dtype_size(out_dtype))};
-    const cuuint32_t box[3] = {32, 32, 1};
+    const cuuint32_t box[3] = {bf16 ? 64u : 32u, 32, 1};   // 128-byte rows
     if ((st = encode_tiled(&p.result, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3,
-                           out, d, st2, box, bf16 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B)) !=
-        MUON_OK)
+                           out, d, st2, box, CU_TENSOR_MAP_SWIZZLE_128B)) != MUON_OK)
       return st;
   }
   p.add = add;

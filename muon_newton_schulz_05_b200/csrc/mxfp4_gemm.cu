@@ -46,7 +46,7 @@ constexpr int kPStages = 5;
 constexpr int kPStageBytes = 2 * kCodeBytes;
 constexpr int kSfSlots = 8;                        // the scales' own ring
 constexpr int kPScaleBytes = 3 * kSfGroupBytes;    // A's 128 rows, B's 256
-constexpr int kPChunkBytes = 32 * 32 * 4;          // an epilogue warp's 32 x 32 chunk
+constexpr int kPChunkBytes = 32 * 128;             // an epilogue warp's buffer: 32 rows of 128 bytes
 constexpr int kPSmemBytes =
     kPStages * kPStageBytes + kSfSlots * kPScaleBytes + kMxEpiWarps * kPChunkBytes + 1024 + 512;
 constexpr uint32_t kAccOffset = 160;               // first column of the second accumulator
@@ -88,40 +88,65 @@ __device__ __forceinline__ MxTile mx_tile(const MxGemmParams& p, int t) {
   return x;
 }
 
-// A warp's 32 x 32 chunk of fp32 results (one row per lane) as one TMA store,
-// through its shared-memory buffer (bf16: two half buffers in turn, 64-byte
-// swizzle; fp32: 128-byte swizzle; conflict-free either way).
-template <bool kBf16>
-__device__ __forceinline__ void store_chunk_tma(const MxGemmParams& p, uint8_t* buf, uint32_t turn, int lane,
-                                                const uint32_t* r, int c, int row, int col) {
-  if (kBf16) buf += (turn & 1u) * 2048;
-  if (lane == 0) bulk_wait_read<kBf16 ? 1 : 0>();   // the store that used this buffer has read it
-  __syncwarp();
-  if (kBf16) {
+// A warp's 32 x 64 bf16 results, two 32 x 32 chunks with one row per lane, into
+// its buffer: rows of 128 bytes, 16-byte group g of row r at g ^ (r & 7) (TMA's
+// 128-byte swizzle; conflict-free by rows and by columns). chunk a is half ha.
+__device__ __forceinline__ void stage_bf16(uint8_t* buf, int lane, const uint32_t* a, int ha, const uint32_t* b) {
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+    const uint32_t* r = c ? b : a;
+    const int h = c ? 1 - ha : ha;
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
       uint32_t w[4];
 #pragma unroll
-      for (int h = 0; h < 4; ++h)
-        w[h] = pack_bf16x2(__uint_as_float(r[8 * g + 2 * h]), __uint_as_float(r[8 * g + 2 * h + 1]));
-      *reinterpret_cast<uint4*>(buf + lane * 64 + ((g ^ ((lane >> 1) & 3)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+      for (int i = 0; i < 4; ++i)
+        w[i] = pack_bf16x2(__uint_as_float(r[8 * g + 2 * i]), __uint_as_float(r[8 * g + 2 * i + 1]));
+      *reinterpret_cast<uint4*>(buf + lane * 128 + (((4 * h + g) ^ (lane & 7)) << 4)) =
+          make_uint4(w[0], w[1], w[2], w[3]);
     }
-  } else {
-#pragma unroll
-    for (int g = 0; g < 8; ++g)
-      *reinterpret_cast<uint4*>(buf + lane * 128 + ((g ^ (lane & 7)) << 4)) =
-          make_uint4(r[4 * g], r[4 * g + 1], r[4 * g + 2], r[4 * g + 3]);
   }
-  fence_proxy_async_smem();
-  __syncwarp();
-  if (lane == 0 && row < p.m && col < p.n) tma_store_3d(&p.result, buf, col, row, c);
-  if (lane == 0) bulk_commit();
 }
 
-// The same for outputs that TMA cannot address, or with an addend: turned in
-// shared memory so that neighbouring lanes store neighbouring columns
-// (16-byte group g of row r lies at g ^ (r & 7)).
+// The pair of chunks by TMA: one store in bf16, two in fp32 (a chunk's rows are
+// 128 bytes there).
 template <bool kBf16>
+__device__ __forceinline__ void store_pair_tma(const MxGemmParams& p, uint8_t* buf, int lane, const uint32_t* a,
+                                               int ha, const uint32_t* b, int c, int row, int col) {
+  const bool rows = row < p.m;
+#pragma unroll
+  for (int t = 0; t < (kBf16 ? 1 : 2); ++t) {
+    const uint32_t* r = t ? b : a;
+    const int at = kBf16 ? col : col + 32 * (t ? 1 - ha : ha);
+    if (lane == 0) bulk_wait_read<0>();   // the store before has read the buffer
+    __syncwarp();
+    if (kBf16) {
+      stage_bf16(buf, lane, a, ha, b);
+    } else {
+#pragma unroll
+      for (int g = 0; g < 8; ++g)
+        *reinterpret_cast<uint4*>(buf + lane * 128 + ((g ^ (lane & 7)) << 4)) =
+            make_uint4(r[4 * g], r[4 * g + 1], r[4 * g + 2], r[4 * g + 3]);
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0 && rows && at < p.n) {
+      tma_store_3d(&p.result, buf, at, row, c);
+      bulk_commit();
+    }
+  }
+}
+
+// A chunk for outputs that TMA cannot address, or with an addend: turned in
+// shared memory (16-byte group g of row r at g ^ (r & 7)) so that neighbouring
+// lanes load and store neighbouring columns, four at a time where rows have a
+// multiple of 4 elements. The addends of the whole chunk are on their way at
+// once; rows past the end repeat the last one. (For rows that start anywhere,
+// 4-byte stores with a shift by one element, and 16-byte pieces with
+// element-wise ends, both took longer: 21.7 and 24.2 against 18.5 us for
+// 4 x 1000 x 1537 x 771. Such rows cost partial sectors either way; 1536
+// columns take 10.3 us.)
+template <bool kBf16, bool kAdd>
 __device__ __forceinline__ void store_chunk(const MxGemmParams& p, uint8_t* buf, int lane, const uint32_t* r,
                                             long long base, int row, int col, bool vec) {
   __syncwarp();   // the previous chunk has been read
@@ -130,67 +155,72 @@ __device__ __forceinline__ void store_chunk(const MxGemmParams& p, uint8_t* buf,
     *reinterpret_cast<uint4*>(buf + lane * 128 + ((g ^ (lane & 7)) << 4)) =
         make_uint4(r[4 * g], r[4 * g + 1], r[4 * g + 2], r[4 * g + 3]);
   __syncwarp();
-  if (vec) {   // rows of a multiple of 4 elements: 8 lanes per row, 4 columns each
+  const int rows = min(32, p.m - row);
+  if (rows <= 0) return;
+  if (vec) {   // 8 lanes per row, 4 columns each
     const int c = col + 4 * (lane & 7);
-    const int rows = c < p.n ? p.m - row : 0;
-    const long long at = base + static_cast<long long>(row + (lane >> 3)) * p.n + c;
-    float4 v[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int rr = 4 * i + (lane >> 3);
-      v[i] = *reinterpret_cast<const float4*>(buf + rr * 128 + (((lane & 7) ^ (rr & 7)) << 4));
-    }
-    if (p.add) {
+    if (c >= p.n) return;
+    const long long at = base + static_cast<long long>(row) * p.n + c;
+    uint4 add[8];   // four values: fp32, or bf16 in x and y
+    if (kAdd) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        if (4 * i + (lane >> 3) < rows) {
-          if (kBf16) {
-            const uint2 a = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(p.add) + at + 4LL * i * p.n);
-            v[i].x += bf16_lo_f(a.x); v[i].y += bf16_hi_f(a.x); v[i].z += bf16_lo_f(a.y); v[i].w += bf16_hi_f(a.y);
-          } else {
-            const float4 a = *reinterpret_cast<const float4*>(static_cast<const float*>(p.add) + at + 4LL * i * p.n);
-            v[i].x += a.x; v[i].y += a.y; v[i].z += a.z; v[i].w += a.w;
-          }
+        const long long e = at + static_cast<long long>(min(4 * i + (lane >> 3), rows - 1)) * p.n;
+        if (kBf16) {
+          const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(p.add) + e);
+          add[i].x = w.x;
+          add[i].y = w.y;
+        } else {
+          add[i] = *reinterpret_cast<const uint4*>(static_cast<const float*>(p.add) + e);
         }
       }
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      if (4 * i + (lane >> 3) < rows) {
-        if (kBf16)
-          *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + at + 4LL * i * p.n) =
-              make_uint2(pack_bf16x2(v[i].x, v[i].y), pack_bf16x2(v[i].z, v[i].w));
-        else
-          *reinterpret_cast<float4*>(static_cast<float*>(p.out) + at + 4LL * i * p.n) = v[i];
+      const int rr = 4 * i + (lane >> 3);
+      float4 v = *reinterpret_cast<const float4*>(buf + rr * 128 + (((lane & 7) ^ (rr & 7)) << 4));
+      const long long e = at + static_cast<long long>(rr) * p.n;
+      if (kBf16) {
+        if (kAdd) {
+          v.x += bf16_lo_f(add[i].x); v.y += bf16_hi_f(add[i].x); v.z += bf16_lo_f(add[i].y); v.w += bf16_hi_f(add[i].y);
+        }
+        if (rr < rows)
+          *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + e) =
+              make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+      } else {
+        if (kAdd) {
+          v.x += __uint_as_float(add[i].x); v.y += __uint_as_float(add[i].y);
+          v.z += __uint_as_float(add[i].z); v.w += __uint_as_float(add[i].w);
+        }
+        if (rr < rows) *reinterpret_cast<float4*>(static_cast<float*>(p.out) + e) = v;
       }
     }
-  } else if (col + lane < p.n) {   // one column per lane; the whole chunk is read before the first store
-    const int rows = min(32, p.m - row);
+  } else if (col + lane < p.n) {   // one column per lane
     const long long at = base + static_cast<long long>(row) * p.n + col + lane;
     float v[32];
 #pragma unroll
     for (int rr = 0; rr < 32; ++rr)
-      v[rr] = *reinterpret_cast<const float*>(buf + rr * 128 + (((lane >> 2) ^ (rr & 7)) << 4) + (lane & 3) * 4);
-    if (p.add) {
+      v[rr] = kAdd ? load1t<kBf16>(p.add, at + static_cast<long long>(min(rr, rows - 1)) * p.n) : 0.0f;
 #pragma unroll
-      for (int rr = 0; rr < 32; ++rr)
-        if (rr < rows) v[rr] += load1t<kBf16>(p.add, at + static_cast<long long>(rr) * p.n);
+    for (int rr = 0; rr < 32; ++rr) {
+      const float y = *reinterpret_cast<const float*>(buf + rr * 128 + (((lane >> 2) ^ (rr & 7)) << 4) + (lane & 3) * 4);
+      v[rr] = kAdd ? v[rr] + y : y;
     }
-    if (rows == 32) {
 #pragma unroll
-      for (int rr = 0; rr < 32; ++rr) store1t<kBf16>(p.out, at + static_cast<long long>(rr) * p.n, v[rr]);
-    } else {
-#pragma unroll
-      for (int rr = 0; rr < 32; ++rr)
-        if (rr < rows) store1t<kBf16>(p.out, at + static_cast<long long>(rr) * p.n, v[rr]);
-    }
+    for (int rr = 0; rr < 32; ++rr)
+      if (rr < rows) store1t<kBf16>(p.out, at + static_cast<long long>(rr) * p.n, v[rr]);
   }
 }
 
 }  // namespace
 
 // ------------------------------------------------------------------ pair kernel
-template <bool kBf16, bool kSplit>
+// How results leave: partial tiles of a split product, TMA stores, or loads and
+// stores of the epilogue warps (out's rows do not start on 16-byte boundaries,
+// or there is an addend). One kernel each: together they spill registers.
+enum PairStore : int { kStoreParts = 0, kStoreTma = 1, kStorePlain = 2, kStoreAdd = 3 };
+
+template <bool kBf16, int kStore>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
     mx_gemm_pair_kernel(const __grid_constant__ MxGemmParams p) {
   extern __shared__ uint8_t smem_raw[];
@@ -421,7 +451,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
     const uint32_t tnext_leader = mapa_shared(smem_u32(tnext), 0);
     const bool vec = (p.n % 4) == 0;
     uint8_t* buf = chunks + (warp - 2) * kPChunkBytes;
-    uint32_t acc = 0, phase = 0, chunk = 0;   // chunk: counts this warp's stores (its half buffers take turns)
+    uint32_t acc = 0, phase = 0;
     bool ok = true;
     for (int t = pair; ok && t < ntiles; t += npairs) {
       const MxTile T = mx_tile(p, t);
@@ -440,41 +470,49 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
       const uint32_t tb = tmem_base + (static_cast<uint32_t>(32 * q) << 16) + acc * kAccOffset + half * 128;
       const int row = T.im * kPTile + kRows * static_cast<int>(rank) + 32 * q;
       const int col = T.in * kPTile + half * 128;
-      auto store = [&](const uint32_t* r, int j) {
-        if (kSplit) {
-          // partial tile: the 32 x 32 chunk as 8 rows of 32 float4, one per lane
-          float4* dst = reinterpret_cast<float4*>(
-              p.part + static_cast<long long>(t) * (kPTile * kPTile) +
-              ((((rank * 4 + q) * 2 + half) * 4 + j) * 1024));
+      auto store_pair = [&](const uint32_t* a, int ha, const uint32_t* b, int j) {   // chunks j + ha, j + 1 - ha
+        if constexpr (kStore == kStoreParts) {
+          // partial tile: a 32 x 32 chunk as 8 rows of 32 float4, one per lane
 #pragma unroll
-          for (int g = 0; g < 8; ++g)
-            dst[g * 32 + lane] = make_float4(__uint_as_float(r[4 * g]), __uint_as_float(r[4 * g + 1]),
-                                             __uint_as_float(r[4 * g + 2]), __uint_as_float(r[4 * g + 3]));
-        } else if (p.tma_out) {
-          store_chunk_tma<kBf16>(p, buf, chunk++, lane, r, T.c, row, col + j * 32);
+          for (int c = 0; c < 2; ++c) {
+            const uint32_t* r = c ? b : a;
+            float4* dst = reinterpret_cast<float4*>(
+                p.part + static_cast<long long>(t) * (kPTile * kPTile) +
+                ((((rank * 4 + q) * 2 + half) * 4 + j + (c ? 1 - ha : ha)) * 1024));
+#pragma unroll
+            for (int g = 0; g < 8; ++g)
+              dst[g * 32 + lane] = make_float4(__uint_as_float(r[4 * g]), __uint_as_float(r[4 * g + 1]),
+                                               __uint_as_float(r[4 * g + 2]), __uint_as_float(r[4 * g + 3]));
+          }
+        } else if constexpr (kStore == kStoreTma) {
+          store_pair_tma<kBf16>(p, buf, lane, a, ha, b, T.c, row, col + j * 32);
         } else {
-          store_chunk<kBf16>(p, buf, lane, r, T.c * p.stride_c, row, col + j * 32, vec);
+          constexpr bool kAdd = kStore == kStoreAdd;
+          store_chunk<kBf16, kAdd>(p, buf, lane, a, T.c * p.stride_c, row, col + (j + ha) * 32, vec);
+          store_chunk<kBf16, kAdd>(p, buf, lane, b, T.c * p.stride_c, row, col + (j + 1 - ha) * 32, vec);
         }
       };
-      uint32_t r[kOverlapChunks * 32];
-      // acc 0 shares its last chunks with the other accumulator, acc 1 its first
-      const int first = overlapped && acc == 0 ? 4 - kOverlapChunks : 0;
-#pragma unroll
-      for (int i = 0; i < kOverlapChunks; ++i)
-        tmem_ld32(tb + (first + i) * 32, *reinterpret_cast<uint32_t(*)[32]>(r + 32 * i));
+      // Three of the warp's four chunks are taken to registers first: with them
+      // the columns that the two accumulators share (the last ones of acc 0,
+      // the first ones of acc 1). They are a whole pair and a chunk of the
+      // other one, whose partner follows.
+      static_assert(kOverlapChunks == 3, "chunks in registers");
+      uint32_t r0[32], r1[32], r2[32];
+      const bool back = overlapped && acc == 0;
+      const int pair0 = back ? 2 : 0, lone = back ? 1 : 2, rest = back ? 0 : 3;
+      tmem_ld32(tb + pair0 * 32, r0);
+      tmem_ld32(tb + pair0 * 32 + 32, r1);
+      tmem_ld32(tb + lone * 32, r2);
       tmem_ld_wait();
       if (overlapped) {
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive_cluster_cta(tnext_leader);
       }
-#pragma unroll
-      for (int i = 0; i < kOverlapChunks; ++i) store(r + 32 * i, first + i);
-      const int rest = first == 0 ? kOverlapChunks : 0;
-      static_assert(kOverlapChunks == 3, "one chunk is left");
-      tmem_ld32(tb + rest * 32, *reinterpret_cast<uint32_t(*)[32]>(r));
+      store_pair(r0, 0, r1, pair0);
+      tmem_ld32(tb + rest * 32, r0);
       tmem_ld_wait();
-      store(r, rest);
+      store_pair(r2, lone & 1 ? 1 : 0, r0, back ? 0 : 2);
       acc ^= 1u;
       if (acc == 0) phase ^= 1u;
     }
@@ -483,7 +521,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
   }
 
   // let the kernel that adds the parts be launched (it waits for this grid)
-  if (kSplit) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (kStore == kStoreParts) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   tc_fence_before();
   __syncthreads();
   cluster_arrive_relaxed();   // no MMA of the pair and no remote signal is still in flight
@@ -869,10 +907,16 @@ MxGemmPlan plan_mx_gemm(const MxGemmShape& s, int pairs, int sms) {
   return pl;
 }
 
-static const void* pair_kernel(bool bf16, bool split) {
-  if (split) return reinterpret_cast<const void*>(&mx_gemm_pair_kernel<false, true>);
-  return bf16 ? reinterpret_cast<const void*>(&mx_gemm_pair_kernel<true, false>)
-              : reinterpret_cast<const void*>(&mx_gemm_pair_kernel<false, false>);
+template <int kStore>
+static const void* pair_kernel_store(bool bf16) {
+  return bf16 ? reinterpret_cast<const void*>(&mx_gemm_pair_kernel<true, kStore>)
+              : reinterpret_cast<const void*>(&mx_gemm_pair_kernel<false, kStore>);
+}
+
+static const void* pair_kernel(bool bf16, int store) {
+  if (store == kStoreParts) return reinterpret_cast<const void*>(&mx_gemm_pair_kernel<false, kStoreParts>);
+  return store == kStoreTma ? pair_kernel_store<kStoreTma>(bf16)
+                            : store == kStorePlain ? pair_kernel_store<kStorePlain>(bf16) : pair_kernel_store<kStoreAdd>(bf16);
 }
 
 template <int NT>
@@ -895,8 +939,9 @@ static int few_smem(const MxGemmPlan& pl) {
 
 cudaError_t mx_gemm_prepare(int* max_pairs) {
   cudaError_t e = cudaSuccess;
-  for (int i = 0; i < 3 && e == cudaSuccess; ++i)
-    e = cudaFuncSetAttribute(pair_kernel(i & 1, i & 2), cudaFuncAttributeMaxDynamicSharedMemorySize, kPSmemBytes);
+  for (int store = kStoreParts; store <= kStoreAdd; ++store)
+    for (int b = 0; b < 2 && e == cudaSuccess; ++b)
+      e = cudaFuncSetAttribute(pair_kernel(b, store), cudaFuncAttributeMaxDynamicSharedMemorySize, kPSmemBytes);
   for (int nt = 16; nt <= 64; nt *= 2)
     for (int b = 0; b < 2 && e == cudaSuccess; ++b)
       e = cudaFuncSetAttribute(few_kernel(nt, b), cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024);
@@ -932,7 +977,8 @@ cudaError_t launch_mx_gemm(const MxGemmParams& p, const MxGemmPlan& plan, bool b
   cfg.gridDim = dim3(2 * pairs, 1, 1);
   cfg.blockDim = dim3(kMxThreads, 1, 1);
   cfg.dynamicSmemBytes = kPSmemBytes;
-  cudaError_t e = cudaLaunchKernelExC(&cfg, pair_kernel(bf16, plan.split > 1), args);
+  const int store = plan.split > 1 ? kStoreParts : p.tma_out ? kStoreTma : p.add ? kStoreAdd : kStorePlain;
+  cudaError_t e = cudaLaunchKernelExC(&cfg, pair_kernel(bf16, store), args);
   if (e != cudaSuccess || plan.split == 1) return e;
   cfg.gridDim = dim3(static_cast<unsigned>(tiles) * 64u, 1, 1);
   cfg.blockDim = dim3(256, 1, 1);
