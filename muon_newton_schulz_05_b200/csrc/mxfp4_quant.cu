@@ -326,7 +326,8 @@ __device__ __forceinline__ void code_rows(const QuantParams& p, uint8_t* tile, u
         for (int t = 0; t < 4; ++t) {
           const bool lo = (uu[t] << 16) >= threshold_hi, hi = uu[t] >= threshold_hi;
           if (C::kHalf) {
-            w[j * kPer + t] &= (lo ? 0xFFFFu : 0u) | (hi ? 0xFFFF0000u : 0u);
+            if (!lo) w[j * kPer + t] &= 0xFFFF0000u;
+            if (!hi) w[j * kPer + t] &= 0xFFFFu;
           } else {
             if (!lo) w[j * kPer + (2 * t) % kPer] = 0u;
             if (!hi) w[j * kPer + (2 * t + 1) % kPer] = 0u;
