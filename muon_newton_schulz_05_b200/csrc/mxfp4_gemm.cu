@@ -233,8 +233,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
   uint64_t* sempty = sfull + kSfSlots;
   uint64_t* sready = sempty + kSfSlots;   // scales in TMEM, one per buffer
   uint64_t* tfull = sready + kSfBufs;     // one per accumulator
-  uint64_t* tnext = tfull + 2;            // the next tile's accumulator is free
-  uint64_t* done = tnext + 1;
+  // the accumulator of the tile after this one is free; one per accumulator,
+  // because a warp may arrive for a tile while a slower one has yet to arrive
+  // for the tile before (but not for the one before that: the MMAs between
+  // waited for it)
+  uint64_t* tnext = tfull + 2;
+  uint64_t* done = tnext + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
@@ -256,7 +260,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
     for (int i = 0; i < kSfBufs; ++i) mbar_init(&sready[i], 2 * kMxScaleWarps);
     mbar_init(&tfull[0], 1);
     mbar_init(&tfull[1], 1);
-    mbar_init(tnext, 2 * kMxEpiWarps);
+    mbar_init(&tnext[0], 2 * kMxEpiWarps);
+    mbar_init(&tnext[1], 2 * kMxEpiWarps);
     mbar_init(done, 1);
     *abort_flag = 0;
     fence_mbar_init();
@@ -323,20 +328,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
         const uint64_t desc0 = smem_desc_sw128(smem_u32(smem), 16, 1024);
         int stage = 0;
         uint32_t phase = 0, uses = 0;
-        uint32_t acc = 0, tfree = 0;
-        bool ok = true, first = true, ready = false;
+        uint32_t tile = 0;   // tiles of this pair so far; their parity is the accumulator
+        bool ok = true, ready = false;
         for (int t = pair; ok && t < ntiles; t += npairs) {
           const int kb0 = p.split == 1 ? 0 : t % p.split * p.kc;
           const int nkb = min(p.kc, p.kstages - kb0);
-          if (!first) {
-            if (!mbar_wait_cluster(tnext, tfree, abort_flag, p.status, limit)) {
-              ok = false;
-              break;
-            }
-            tfree ^= 1u;
+          if (tile > 0 && !mbar_wait_cluster(&tnext[(tile - 1) & 1u], ((tile - 1) >> 1) & 1u, abort_flag, p.status,
+                                             limit)) {
+            ok = false;
+            break;
           }
-          first = false;
-          const uint32_t d = tmem_base + acc * kAccOffset;
+          const uint32_t d = tmem_base + (tile & 1u) * kAccOffset;
           for (int kb = 0; kb < nkb; ++kb) {
             const uint32_t buf = uses % kSfBufs;
             if (!ready &&
@@ -364,8 +366,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
             umma_commit_pair(const_cast<uint64_t*>(used));
           }
           if (!ok) break;
-          umma_commit_pair(&tfull[acc]);
-          acc ^= 1u;
+          umma_commit_pair(&tfull[tile & 1u]);
+          ++tile;
         }
         umma_commit_pair(done);
       }
@@ -459,7 +461,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
       if (!overlapped) {  // this warp holds nothing the next tile's MMAs would overwrite
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster_cta(tnext_leader);
+        if (lane == 0) mbar_arrive_cluster_cta(tnext_leader + 8u * acc);
       }
       const bool got = mbar_wait_cluster(&tfull[acc], phase, abort_flag, p.status, limit);
       if (!__all_sync(0xffffffffu, got)) {
@@ -507,7 +509,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
       if (overlapped) {
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster_cta(tnext_leader);
+        if (lane == 0) mbar_arrive_cluster_cta(tnext_leader + 8u * acc);
       }
       store_pair(r0, 0, r1, pair0);
       tmem_ld32(tb + rest * 32, r0);

@@ -274,7 +274,9 @@ FEW = [(1, 1, 1, 1), (1, 1, 128, 32), (1, 1, 1000, 96), (1, 3, 129, 257), (2, 16
        (1, 33, 500, 1000), (3, 64, 200, 800), (1, 128, 400, 1100), (1, 300, 5, 640), (1, 100, 100, 1800),
        (1, 7, 2000, 1024), (1, 2, 60, 1664)]
 PAIR = [(1, 129, 129, 64), (1, 256, 256, 256), (1, 300, 200, 520), (2, 257, 511, 300), (1, 1000, 771, 1001),
-        (1, 512, 512, 1800), (4, 130, 260, 96), (1, 2600, 2600, 160), (1, 5000, 2048, 320)]
+        (1, 512, 512, 1800), (4, 130, 260, 96), (1, 2600, 2600, 160), (1, 5000, 2048, 320),
+        # many tiles per CTA pair with one K stage each: the epilogue is behind the MMAs all the time
+        (1, 6000, 6016, 64), (1, 5000, 5001, 32)]
 
 
 def _want(a, b):
@@ -428,3 +430,111 @@ def test_bounded_wait_limit_is_not_reached(mb):
         out = torch.empty(1, m, 300, device="cuda")
         mb.mxfp4_matmul(qa, qb, out, ws)
     assert mb.device_status(ws) == 0
+
+
+# --------------------------------------------------- offsets past 32 bits, graphs
+def _rows_numbers(key, site, domain, rows, cols):
+    """16-bit numbers of some rows (indices) of a matrix."""
+    out = np.empty((len(rows), cols), dtype=np.int64)
+    n = (key[1] + site) % 2 ** 64
+    for i, r in enumerate(rows):
+        for g in range((cols + 7) // 8):
+            w = ref.philox([g, int(r), n & ref.M32, (n >> 32) & 0x3FFFFFFF | domain << 30],
+                           [key[0] & ref.M32, key[0] >> 32])
+            for c in range(8 * g, min(cols, 8 * g + 8)):
+                v = w[(c & 7) >> 1]
+                out[i, c] = v >> 16 if c & 1 else v & 0xFFFF
+    return out
+
+
+@pytest.mark.parametrize("cols", [520, 523])
+def test_elements_past_32_bits(mb, cols):
+    """More than 2^31 elements (and, read back in fp32, 2^33 bytes): the last rows,
+    and those around the 2^31st element, of dropout, quantisation and read-back."""
+    rows = (1 << 31) // cols + 300
+    base = _source(64, cols, "bf16", 51).cuda()
+    x = base.repeat(-(-rows // 64), 1)[:rows].contiguous()
+    assert x.numel() > 1 << 31
+    rng, key = _rng(17, 23)
+    probe = [0, (1 << 31) // cols - 1, (1 << 31) // cols, (1 << 31) // cols + 1, rows - 1]
+    out = torch.empty_like(x)
+    mb.dropout(x, out, 0.25, rng)
+    keep = _rows_numbers(key, 0, 0, probe, cols) >= 16384
+    want = np.where(keep, _f64(x[probe]) * (4.0 / 3.0), 0.0)
+    assert np.all(np.abs(_f64(out[probe]) - want) <= np.abs(want) * 2.0 ** -8 * 1.001)
+    del out
+    q, qt = mb.alloc_mxfp4((rows, cols)), mb.alloc_mxfp4((cols, rows))
+    mb.mxfp4_quantize(x, q, qt)
+    back = torch.empty((rows, cols), dtype=torch.bfloat16, device="cuda")
+    mb.mxfp4_dequantize(q, back)
+    codes, scales = ref.quantize(_f64(x[probe]))
+    assert np.array_equal(_f64(back[probe]), ref.values(codes, scales, cols))
+    back = back.view(cols, rows)
+    mb.mxfp4_dequantize(qt, back)
+    tail = _f64(x[rows - rows % 32 - 64:, [0, cols - 1]]).T       # the last blocks of the first and last column
+    codes, scales = ref.quantize(tail)
+    got = _f64(back[[0, cols - 1], rows - rows % 32 - 64:])
+    assert np.array_equal(got, ref.values(codes, scales, tail.shape[1]))
+
+
+@pytest.mark.parametrize("n", [46400, 46399])
+def test_product_past_32_bits(mb, n):
+    """More than 2^31 results."""
+    m = 46500
+    qa, a = _operand(mb, 1, 128, 64, 61)
+    rep = -(-m // 128)
+    big_a = mb.Mxfp4(qa.data.repeat(1, rep, 1)[:, :m].contiguous(), qa.scales.view(-1).repeat(rep), (1, m, 64))
+    rep = -(-n // 128)
+    big_b = mb.Mxfp4(qa.data.repeat(1, rep, 1)[:, :n].contiguous(), qa.scales.view(-1).repeat(rep), (1, n, 64))
+    out = torch.full((m, n), float("nan"), dtype=torch.bfloat16, device="cuda")
+    ws = mb.alloc_matmul_workspace((1, m, 64), (1, n, 64))
+    mb.mxfp4_matmul(big_a, big_b, out, ws)
+    want = torch.from_numpy(_want(a, a))[0].bfloat16().cuda()
+    cols = torch.arange(n, device="cuda") % 128
+    for r in (0, (1 << 31) // n, (1 << 31) // n + 1, m - 1):
+        assert torch.equal(out[r], want[r % 128, cols])
+    assert not bool(torch.isnan(out).any())
+
+
+def test_two_captured_graphs_replayed_at_once(mb):
+    """Split and few-row products captured into two graphs with workspaces of
+    their own and replayed on two streams."""
+    graphs, outs, wants = [], [], []
+    for i, (m, n, k) in enumerate(((300, 260, 16384), (16, 900, 8192))):
+        qa, _ = _operand(mb, 1, m, k, 70 + i, 122, 130)
+        qb, _ = _operand(mb, 1, n, k, 80 + i, 122, 130)
+        ws = mb.alloc_matmul_workspace(qa.shape, qb.shape)
+        out = torch.empty(1, m, n, device="cuda")
+        mb.mxfp4_matmul(qa, qb, out, ws)
+        torch.cuda.synchronize()
+        wants.append(out.clone())
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            for _ in range(4):
+                mb.mxfp4_matmul(qa, qb, out, ws)
+        graphs.append((g, qa, qb, ws))
+        outs.append(out)
+    streams = [torch.cuda.Stream() for _ in graphs]
+    for _ in range(10):
+        for s, g, o in zip(streams, graphs, outs):
+            with torch.cuda.stream(s):
+                o.zero_()
+                g[0].replay()
+    torch.cuda.synchronize()
+    for o, w, g in zip(outs, wants, graphs):
+        assert torch.equal(o, w) and mb.device_status(g[3]) == 0
+
+
+def test_a_matrix_times_itself(mb):
+    """One handle as both operands, and many small matrices in one call."""
+    qa, a = _operand(mb, 1, 300, 200, 91)
+    ws = mb.alloc_matmul_workspace(qa.shape, qa.shape)
+    out = torch.empty(300, 300, device="cuda")
+    mb.mxfp4_matmul(qa, qa, out, ws)
+    assert np.array_equal(_f64(out), _want(a, a)[0])
+    qb, b = _operand(mb, 700, 3, 40, 92)
+    qc, c = _operand(mb, 700, 5, 40, 93)
+    ws = mb.alloc_matmul_workspace(qb.shape, qc.shape)
+    out = torch.empty(700, 3, 5, dtype=torch.bfloat16, device="cuda")
+    mb.mxfp4_matmul(qb, qc, out, ws)
+    assert torch.equal(out.cpu(), torch.from_numpy(_want(b, c)).bfloat16())
