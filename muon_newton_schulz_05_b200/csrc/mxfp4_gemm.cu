@@ -298,7 +298,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
         const int lrow = T.im * kPTile + kRows * static_cast<int>(rank);
         const int rrow = T.in * kPTile + kRows * static_cast<int>(rank);
         for (int kb = 0; kb < T.nkb; ++kb) {
-          if (!mbar_wait_cluster(&empty[stage], phase ^ 1u, abort_flag, p.status, limit)) {
+          if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag, p.status, limit)) {
             ok = false;
             break;
           }
@@ -333,7 +333,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
         for (int t = pair; ok && t < ntiles; t += npairs) {
           const int kb0 = p.split == 1 ? 0 : t % p.split * p.kc;
           const int nkb = min(p.kc, p.kstages - kb0);
-          if (tile > 0 && !mbar_wait_cluster(&tnext[(tile - 1) & 1u], ((tile - 1) >> 1) & 1u, abort_flag, p.status,
+          if (tile > 0 && !mbar_wait(&tnext[(tile - 1) & 1u], ((tile - 1) >> 1) & 1u, abort_flag, p.status,
                                              limit)) {
             ok = false;
             break;
@@ -342,8 +342,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
           for (int kb = 0; kb < nkb; ++kb) {
             const uint32_t buf = uses % kSfBufs;
             if (!ready &&
-                (!mbar_wait_cluster(&full[stage], phase, abort_flag, p.status, limit) ||
-                 !mbar_wait_cluster(&sready[buf], (uses / kSfBufs) & 1u, abort_flag, p.status, limit))) {
+                (!mbar_wait(&full[stage], phase, abort_flag, p.status, limit) ||
+                 !mbar_wait(&sready[buf], (uses / kSfBufs) & 1u, abort_flag, p.status, limit))) {
               ok = false;
               break;
             }
@@ -360,8 +360,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
                 umma_mxf4_pair(d, a + 2 * ks, b + 2 * ks, idesc_mxf4(kPTile, kPTile, 2 * (ks & 1)),
                                sfa + 4 * (ks >> 1), sfb + 8 * (ks >> 1), (kb > 0 || ks > 0) ? 1u : 0u);
               if (ks == 1)
-                ready = mbar_test_cluster(&full[stage], phase) &&
-                        mbar_test_cluster(&sready[uses % kSfBufs], (uses / kSfBufs) & 1u);
+                ready = mbar_test(&full[stage], phase) &&
+                        mbar_test(&sready[uses % kSfBufs], (uses / kSfBufs) & 1u);
             }
             umma_commit_pair(const_cast<uint64_t*>(used));
           }
@@ -426,7 +426,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
         // a buffer is free once the MMAs that used it are done
         if (uses >= kSfBufs &&
             !__all_sync(0xffffffffu,
-                        mbar_wait_cluster(&empty[old_stage], old_phase, abort_flag, p.status, limit))) {
+                        mbar_wait(&empty[old_stage], old_phase, abort_flag, p.status, limit))) {
           ok = false;
           break;
         }
@@ -463,7 +463,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive_cluster_cta(tnext_leader + 8u * acc);
       }
-      const bool got = mbar_wait_cluster(&tfull[acc], phase, abort_flag, p.status, limit);
+      const bool got = mbar_wait(&tfull[acc], phase, abort_flag, p.status, limit);
       if (!__all_sync(0xffffffffu, got)) {
         ok = false;
         break;

@@ -44,13 +44,12 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void*
       : "memory");
 }
 
-// Non-blocking: has the barrier phase of `parity` completed (cluster-scope
-// acquire)?
-__device__ __forceinline__ bool mbar_test_cluster(const uint64_t* bar, uint32_t parity) {
+// Non-blocking: has the barrier phase of `parity` completed?
+__device__ __forceinline__ bool mbar_test(const uint64_t* bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
-      "mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
       "selp.u32 %0, 1, 0, p;\n\t}\n"
       : "=r"(ok)
       : "r"(smem_u32(bar)), "r"(parity)
