@@ -227,12 +227,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* slots = smem + kPStages * kPStageBytes;
   uint8_t* chunks = slots + kSfSlots * kPScaleBytes;
-  uint64_t* full = reinterpret_cast<uint64_t*>(chunks + kMxEpiWarps * kPChunkBytes);  // codes, both CTAs'
+  // both CTAs' codes in shared memory and scales in TMEM
+  uint64_t* full = reinterpret_cast<uint64_t*>(chunks + kMxEpiWarps * kPChunkBytes);
   uint64_t* empty = full + kPStages;
   uint64_t* sfull = empty + kPStages;     // scales in shared memory, this CTA's
   uint64_t* sempty = sfull + kSfSlots;
-  uint64_t* sready = sempty + kSfSlots;   // scales in TMEM, one per buffer
-  uint64_t* tfull = sready + kSfBufs;     // one per accumulator
+  uint64_t* tfull = sempty + kSfSlots;    // one per accumulator
   // the accumulator of the tile after this one is free; one per accumulator,
   // because a warp may arrive for a tile while a slower one has yet to arrive
   // for the tile before (but not for the one before that: the MMAs between
@@ -250,14 +250,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kPStages; ++s) {
-      mbar_init(&full[s], 1);
+      mbar_init(&full[s], 1 + 2 * kMxScaleWarps);
       mbar_init(&empty[s], 1);
     }
     for (int s = 0; s < kSfSlots; ++s) {
       mbar_init(&sfull[s], 1);
       mbar_init(&sempty[s], kMxScaleWarps);
     }
-    for (int i = 0; i < kSfBufs; ++i) mbar_init(&sready[i], 2 * kMxScaleWarps);
     mbar_init(&tfull[0], 1);
     mbar_init(&tfull[1], 1);
     mbar_init(&tnext[0], 2 * kMxEpiWarps);
@@ -318,61 +317,58 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
           if (issued[s] >= 0) drain(&full[s], static_cast<uint32_t>(issued[s]), limit);
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      if (rank == 0) {
-        // -------------------------------------------------- MMA issuer (leader)
-        // The tensor pipe holds few MMAs, so the time between the last one of a
-        // stage and the first one of the next must be short: the next stage's
-        // barriers are looked at in the middle of this one, and descriptors
-        // differ by additions only (K step: 32 bytes, stage: kPStageBytes).
-        const uint64_t desc0 = smem_desc_sw128(smem_u32(smem), 16, 1024);
-        int stage = 0;
-        uint32_t phase = 0, uses = 0;
-        uint32_t tile = 0;   // tiles of this pair so far; their parity is the accumulator
-        bool ok = true, ready = false;
-        for (int t = pair; ok && t < ntiles; t += npairs) {
-          const int kb0 = p.split == 1 ? 0 : t % p.split * p.kc;
-          const int nkb = min(p.kc, p.kstages - kb0);
-          if (tile > 0 && !mbar_wait(&tnext[(tile - 1) & 1u], ((tile - 1) >> 1) & 1u, abort_flag, p.status,
-                                             limit)) {
+    if (rank == 0 && lane == 0) {
+      // -------------------------------------------------- MMA issuer (leader)
+      // Four MMAs take the tensor pipe 512 cycles, and this thread's work per
+      // stage must take less: one barrier per stage (codes and scales arrive on
+      // the same one), asked for the next stage before this one's MMAs and
+      // looked at after them, and descriptors that differ by additions only
+      // (K step: 32 bytes, stage: kPStageBytes).
+      const uint64_t desc0 = smem_desc_sw128(smem_u32(smem), 16, 1024);
+      constexpr uint32_t id0 = idesc_mxf4(kPTile, kPTile, 0), id2 = idesc_mxf4(kPTile, kPTile, 2);
+      int stage = 0;
+      uint32_t phase = 0, uses = 0;
+      uint32_t tile = 0;   // tiles of this pair so far; their parity is the accumulator
+      bool ok = true, ready = false;
+      for (int t = pair; ok && t < ntiles; t += npairs) {
+        const int kb0 = p.split == 1 ? 0 : t % p.split * p.kc;
+        const int nkb = min(p.kc, p.kstages - kb0), tail = p.k64 - 4 * (kb0 + nkb - 1);   // K steps of the last stage
+        if (tile > 0 && !mbar_wait(&tnext[(tile - 1) & 1u], ((tile - 1) >> 1) & 1u, abort_flag, p.status, limit)) {
+          ok = false;
+          break;
+        }
+        const uint32_t d = tmem_base + (tile & 1u) * kAccOffset;
+        for (int kb = 0; kb < nkb; ++kb) {
+          if (!ready && !mbar_wait(&full[stage], phase, abort_flag, p.status, limit)) {
             ok = false;
             break;
           }
-          const uint32_t d = tmem_base + (tile & 1u) * kAccOffset;
-          for (int kb = 0; kb < nkb; ++kb) {
-            const uint32_t buf = uses % kSfBufs;
-            if (!ready &&
-                (!mbar_wait(&full[stage], phase, abort_flag, p.status, limit) ||
-                 !mbar_wait(&sready[buf], (uses / kSfBufs) & 1u, abort_flag, p.status, limit))) {
-              ok = false;
-              break;
-            }
-            tc_fence_after();
-            const uint64_t a = desc0 + static_cast<uint32_t>(stage * (kPStageBytes >> 4)), b = a + (kCodeBytes >> 4);
-            const uint32_t sfa = tmem_base + kSfColumn + buf * kSfBuf, sfb = sfa + 8;
-            const int steps = min(4, p.k64 - 4 * (kb0 + kb));
-            const uint64_t* used = &empty[stage];
-            ++uses;
-            if (++stage == kPStages) { stage = 0; phase ^= 1u; }
-#pragma unroll
-            for (int ks = 0; ks < 4; ++ks) {
-              if (ks < steps)
-                umma_mxf4_pair(d, a + 2 * ks, b + 2 * ks, idesc_mxf4(kPTile, kPTile, 2 * (ks & 1)),
-                               sfa + 4 * (ks >> 1), sfb + 8 * (ks >> 1), (kb > 0 || ks > 0) ? 1u : 0u);
-              if (ks == 1)
-                ready = mbar_test(&full[stage], phase) &&
-                        mbar_test(&sready[uses % kSfBufs], (uses / kSfBufs) & 1u);
-            }
-            umma_commit_pair(const_cast<uint64_t*>(used));
+          tc_fence_after();
+          const uint64_t a = desc0 + static_cast<uint32_t>(stage * (kPStageBytes >> 4)), b = a + (kCodeBytes >> 4);
+          const uint32_t sfa = tmem_base + kSfColumn + uses % kSfBufs * kSfBuf, sfb = sfa + 8;
+          uint64_t* used = &empty[stage];
+          ++uses;
+          if (++stage == kPStages) { stage = 0; phase ^= 1u; }
+          ready = mbar_test(&full[stage], phase);
+          umma_mxf4_pair(d, a, b, id0, sfa, sfb, kb > 0 ? 1u : 0u);
+          if (kb + 1 < nkb || tail >= 4) {
+            umma_mxf4_pair(d, a + 2, b + 2, id2, sfa, sfb, 1u);
+            umma_mxf4_pair(d, a + 4, b + 4, id0, sfa + 4, sfb + 8, 1u);
+            umma_mxf4_pair(d, a + 6, b + 6, id2, sfa + 4, sfb + 8, 1u);
+          } else {   // the end of K
+            if (tail > 1) umma_mxf4_pair(d, a + 2, b + 2, id2, sfa, sfb, 1u);
+            if (tail > 2) umma_mxf4_pair(d, a + 4, b + 4, id0, sfa + 4, sfb + 8, 1u);
           }
-          if (!ok) break;
-          umma_commit_pair(&tfull[tile & 1u]);
-          ++tile;
+          umma_commit_pair(used);
         }
-        umma_commit_pair(done);
+        if (!ok) break;
+        umma_commit_pair(&tfull[tile & 1u]);
+        ++tile;
       }
-      drain(done, 0, limit);
+      umma_commit_pair(done);
     }
+    if (lane == 0) drain(done, 0, limit);
+    __syncwarp();
   } else if (warp == 2 + kMxEpiWarps + kMxScaleWarps) {
     if (lane == 0) {
       // ---------------------------------------------------- scale producer
@@ -406,8 +402,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
     // Word j of lane l of a scale tile belongs to row 32 j + l: that is TMEM
     // column j, the same in all four lane quadrants (one per warp).
     const uint32_t quad = static_cast<uint32_t>(32 * (warp & 3)) << 16;
-    const uint32_t ready_leader = mapa_shared(smem_u32(sready), 0);
-    int old_stage = kPStages - kSfBufs, slot = 0;   // old_stage: the one used kSfBufs stages ago
+    const uint32_t full_leader = mapa_shared(smem_u32(full), 0);
+    // stage: the one these scales go with; old_stage: the one used kSfBufs stages before
+    int stage = 0, old_stage = kPStages - kSfBufs, slot = 0;
     uint32_t phase = 0, old_phase = 1, uses = 0;
     bool ok = true;
     for (int t = pair; ok && t < ntiles; t += npairs) {
@@ -438,8 +435,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster_cta(ready_leader + 8u * buf);
+        if (lane == 0) mbar_arrive_cluster_cta(full_leader + 8u * static_cast<uint32_t>(stage));
         ++uses;
+        if (++stage == kPStages) stage = 0;
         if (++slot == kSfSlots) { slot = 0; phase ^= 1u; }
         if (++old_stage == kPStages) { old_stage = 0; old_phase ^= 1u; }
       }
