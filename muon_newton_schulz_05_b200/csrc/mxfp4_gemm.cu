@@ -317,55 +317,71 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
           if (issued[s] >= 0) drain(&full[s], static_cast<uint32_t>(issued[s]), limit);
     }
   } else if (warp == 1) {
-    if (rank == 0 && lane == 0) {
+    if (rank == 0) {
       // -------------------------------------------------- MMA issuer (leader)
-      // Four MMAs take the tensor pipe 512 cycles, and this thread's work per
+      // Four MMAs take the tensor pipe 512 cycles, and this warp's work per
       // stage must take less: one barrier per stage (codes and scales arrive on
       // the same one), asked for the next stage before this one's MMAs and
-      // looked at after them, and descriptors that differ by additions only
-      // (K step: 32 bytes, stage: kPStageBytes).
+      // looked at after them; the whole warp runs the loop, so that addresses
+      // and descriptors are uniform values, and they change by additions only
+      // (K step: 32 bytes, stage: kPStageBytes). Lane 0 issues.
       const uint64_t desc0 = smem_desc_sw128(smem_u32(smem), 16, 1024);
+      constexpr uint32_t kStageStep = kPStageBytes >> 4, kOperandB = kCodeBytes >> 4;
       constexpr uint32_t id0 = idesc_mxf4(kPTile, kPTile, 0), id2 = idesc_mxf4(kPTile, kPTile, 2);
-      int stage = 0;
-      uint32_t phase = 0, uses = 0;
+      const bool issuer = lane == 0;
+      const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_base, 0), sf0 = tmem + kSfColumn;
+      const uint32_t full0 = smem_u32(full), empty0 = smem_u32(empty);
+      uint32_t stage = 0, phase = 0, sf = 0;   // sf: scale column of the stage
+      uint64_t a = desc0;
       uint32_t tile = 0;   // tiles of this pair so far; their parity is the accumulator
       bool ok = true, ready = false;
       for (int t = pair; ok && t < ntiles; t += npairs) {
         const int kb0 = p.split == 1 ? 0 : t % p.split * p.kc;
         const int nkb = min(p.kc, p.kstages - kb0), tail = p.k64 - 4 * (kb0 + nkb - 1);   // K steps of the last stage
-        if (tile > 0 && !mbar_wait(&tnext[(tile - 1) & 1u], ((tile - 1) >> 1) & 1u, abort_flag, p.status, limit)) {
+        if (tile > 0 && !__all_sync(0xffffffffu, mbar_wait(&tnext[(tile - 1) & 1u], ((tile - 1) >> 1) & 1u,
+                                                           abort_flag, p.status, limit))) {
           ok = false;
           break;
         }
-        const uint32_t d = tmem_base + (tile & 1u) * kAccOffset;
+        const uint32_t d = tmem + (tile & 1u) * kAccOffset;
+        uint32_t accumulate = 0;
+#pragma unroll 1
         for (int kb = 0; kb < nkb; ++kb) {
-          if (!ready && !mbar_wait(&full[stage], phase, abort_flag, p.status, limit)) {
+          if (!ready && !__all_sync(0xffffffffu, mbar_wait(&full[stage], phase, abort_flag, p.status, limit))) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint64_t a = desc0 + static_cast<uint32_t>(stage * (kPStageBytes >> 4)), b = a + (kCodeBytes >> 4);
-          const uint32_t sfa = tmem_base + kSfColumn + uses % kSfBufs * kSfBuf, sfb = sfa + 8;
-          uint64_t* used = &empty[stage];
-          ++uses;
-          if (++stage == kPStages) { stage = 0; phase ^= 1u; }
-          ready = mbar_test(&full[stage], phase);
-          umma_mxf4_pair(d, a, b, id0, sfa, sfb, kb > 0 ? 1u : 0u);
-          if (kb + 1 < nkb || tail >= 4) {
-            umma_mxf4_pair(d, a + 2, b + 2, id2, sfa, sfb, 1u);
-            umma_mxf4_pair(d, a + 4, b + 4, id0, sfa + 4, sfb + 8, 1u);
-            umma_mxf4_pair(d, a + 6, b + 6, id2, sfa + 4, sfb + 8, 1u);
-          } else {   // the end of K
-            if (tail > 1) umma_mxf4_pair(d, a + 2, b + 2, id2, sfa, sfb, 1u);
-            if (tail > 2) umma_mxf4_pair(d, a + 4, b + 4, id0, sfa + 4, sfb + 8, 1u);
+          const uint64_t a0 = a;
+          const uint32_t sfa = sf0 + sf, sfb = sfa + 8, used = empty0 + 8u * stage;
+          const bool whole = kb + 1 < nkb || tail >= 4;
+          a += kStageStep;
+          sf = sf == (kSfBufs - 1) * kSfBuf ? 0u : sf + kSfBuf;
+          if (++stage == kPStages) { stage = 0; phase ^= 1u; a = desc0; }
+          const bool next = mbar_test(full0 + 8u * stage, phase);
+          if (whole) {
+            if (issuer) {
+              umma_mxf4_pair(d, a0, a0 + kOperandB, id0, sfa, sfb, accumulate);
+              umma_mxf4_pair(d, a0 + 2, a0 + kOperandB + 2, id2, sfa, sfb, 1u);
+              umma_mxf4_pair(d, a0 + 4, a0 + kOperandB + 4, id0, sfa + 4, sfb + 8, 1u);
+              umma_mxf4_pair(d, a0 + 6, a0 + kOperandB + 6, id2, sfa + 4, sfb + 8, 1u);
+              umma_commit_pair(used);
+            }
+          } else if (issuer) {   // the end of K
+            umma_mxf4_pair(d, a0, a0 + kOperandB, id0, sfa, sfb, accumulate);
+            if (tail > 1) umma_mxf4_pair(d, a0 + 2, a0 + kOperandB + 2, id2, sfa, sfb, 1u);
+            if (tail > 2) umma_mxf4_pair(d, a0 + 4, a0 + kOperandB + 4, id0, sfa + 4, sfb + 8, 1u);
+            umma_commit_pair(used);
           }
-          umma_commit_pair(used);
+          accumulate = 1;
+          ready = __all_sync(0xffffffffu, next);
         }
         if (!ok) break;
-        umma_commit_pair(&tfull[tile & 1u]);
+        if (issuer) umma_commit_pair(&tfull[tile & 1u]);
         ++tile;
       }
-      umma_commit_pair(done);
+      if (issuer) umma_commit_pair(done);
+      __syncwarp();
     }
     if (lane == 0) drain(done, 0, limit);
     __syncwarp();
