@@ -426,7 +426,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
     for (int t = pair; ok && t < ntiles; t += npairs) {
       const MxTile T = mx_tile(p, t);
       for (int kb = 0; kb < T.nkb; ++kb) {
-        // the scales have landed; take them to registers and free the slot
+        // the scales have landed
         if (!__all_sync(0xffffffffu, mbar_wait(&sfull[slot], phase, abort_flag, p.status, limit))) {
           ok = false;
           break;
@@ -434,8 +434,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
         const uint4* sf = reinterpret_cast<const uint4*>(slots + slot * kPScaleBytes) + lane;
         // a 512-byte tile is 32 uint4; A: K halves 0, 1; B: row tile 0 halves 0, 1, row tile 1 halves 0, 1
         const uint4 a0 = sf[0], a1 = sf[32], b00 = sf[64], b01 = sf[96], b10 = sf[128], b11 = sf[160];
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sempty[slot]);
         // a buffer is free once the MMAs that used it are done
         if (uses >= kSfBufs &&
             !__all_sync(0xffffffffu,
@@ -451,7 +449,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster_cta(full_leader + 8u * static_cast<uint32_t>(stage));
+        if (lane == 0) {
+          // the slot goes back only now that its values have been used: an
+          // arrival right behind the loads lets the refill overtake them
+          mbar_arrive(&sempty[slot]);
+          mbar_arrive_cluster_cta(full_leader + 8u * static_cast<uint32_t>(stage));
+        }
         ++uses;
         if (++stage == kPStages) stage = 0;
         if (++slot == kSfSlots) { slot = 0; phase ^= 1u; }

@@ -306,6 +306,36 @@ def test_matmul_is_exact(mb, shape, dtype):
     assert torch.equal(inplace.cpu(), both) and mb.device_status(ws) == 0
 
 
+@pytest.mark.parametrize("shape", [(1, 4096, 4096, 1792), (1, 8192, 2560, 1024), (16, 1024, 768, 768), (1, 16, 8192, 1792)], ids=str)
+def test_repeated_products_are_bitwise_right(mb, shape):
+    """The same large product many times, with scales that differ from row to row
+    and block to block: no call may read a scale or a code too early or too late."""
+    c, m, n, k = shape
+    g = torch.Generator(device="cuda").manual_seed(7)
+
+    def operand(rows):
+        data = torch.randint(0, 256, (c, rows, k // 2), generator=g, device="cuda", dtype=torch.int64).to(torch.uint8)
+        tiles = (c, -(-rows // 128), -(-k // 128), 512)
+        scales = torch.randint(126, 129, tiles, generator=g, device="cuda", dtype=torch.int64).to(torch.uint8)
+        return mb.Mxfp4(data, scales, (c, rows, k))
+    qa, qb = operand(m), operand(n)
+    a, b = torch.empty(c, m, k, device="cuda"), torch.empty(c, n, k, device="cuda")
+    mb.mxfp4_dequantize(qa, a)
+    mb.mxfp4_dequantize(qb, b)
+    # sums of 2^-4 units below 2^24 of them are exact in fp32
+    assert float((a.abs().double() @ b.abs().double().transpose(1, 2)).max()) * 16 < 2 ** 24
+    want = (a.double() @ b.double().transpose(1, 2)).float()
+    ws = mb.alloc_matmul_workspace(qa.shape, qb.shape)
+    for dt in (torch.float32, torch.bfloat16):
+        w = want.to(dt)
+        out = torch.empty(c, m, n, dtype=dt, device="cuda")
+        for i in range(60):
+            out.fill_(float("nan"))
+            mb.mxfp4_matmul(qa, qb, out, ws)
+            assert torch.equal(out, w), i
+    assert mb.device_status(ws) == 0
+
+
 LONG = [(1, 200, 200, 16384), (1, 64, 768, 20000), (2, 150, 300, 9000), (1, 768, 768, 32768), (1, 1, 300, 40000)]
 
 
