@@ -253,7 +253,8 @@ muon_status muon_dropout(const void* x, const void* residual, void* out, int32_t
  * one read of x. The scale is the smallest power of two (at least 2^-127) with
  * amax / scale <= 6, so nothing saturates. stochastic = 0 rounds to nearest,
  * ties to the even code; 1 rounds to one of the two neighbours with the
- * probabilities that keep the mean, out and out_t independently. p > 0 first
+ * probabilities that keep the mean (to 2^-17 of their distance), out and out_t
+ * independently. p > 0 first
  * applies muon_dropout's mask and factor (x as [count * rows][cols]). rng is
  * needed for p > 0 and for stochastic rounding, else NULL. A block with an
  * infinity or a NaN stands for NaN. */
@@ -282,7 +283,8 @@ size_t muon_mxfp4_matmul_workspace_size(int64_t count, int64_t m, int64_t n, int
  * (count 1) that serves every product. fp32 accumulation, one rounding. out
  * may be add itself; it must not overlap add otherwise, nor a, b or the
  * workspace. A device-side wait that ran out is recorded in ws's status word
- * (muon_device_status); out is then incomplete. */
+ * (muon_device_status); out is then incomplete, and until the word is cleared
+ * products that are split along k leave out as it was. */
 muon_status muon_mxfp4_matmul(const muon_mxfp4* a, const muon_mxfp4* b, const void* add, void* out,
                               int32_t out_dtype, void* ws, size_t ws_bytes, void* stream);
 

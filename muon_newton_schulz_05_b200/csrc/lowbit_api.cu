@@ -150,6 +150,7 @@ constexpr int kPlanSms = 148;
 
 MxGemmPlan plan_for(const MxGemmShape& s) { return plan_mx_gemm(s, kPlanSms / 2, kPlanSms); }
 
+// Tensor maps of an operand's codes and, unless tile_box is 0, of its scale tiles.
 muon_status operand_maps(const muon_mxfp4* q, int row_box, int tile_box, CUtensorMap* rows, CUtensorMap* scales) {
   const int64_t blocks = ceil_div(q->cols, kMxBlock), groups = ceil_div(blocks, 4);
   const cuuint64_t rd[3] = {static_cast<cuuint64_t>(blocks * 16), static_cast<cuuint64_t>(q->rows),
@@ -158,7 +159,7 @@ muon_status operand_maps(const muon_mxfp4* q, int row_box, int tile_box, CUtenso
   const cuuint32_t rb[3] = {128, static_cast<cuuint32_t>(row_box), 1};
   muon_status st = encode_tiled(rows, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, q->data, rd, rs, rb,
                                 CU_TENSOR_MAP_SWIZZLE_128B);
-  if (st != MUON_OK) return st;
+  if (st != MUON_OK || tile_box == 0) return st;
   const cuuint64_t sd[2] = {static_cast<cuuint64_t>(groups * (kMxTileBytes / 4)),
                             static_cast<cuuint64_t>(q->count * ceil_div(q->rows, kMxTile))};
   const cuuint64_t ss[1] = {static_cast<cuuint64_t>(groups * kMxTileBytes)};
@@ -303,8 +304,8 @@ muon_status muon_mxfp4_matmul(const muon_mxfp4* a, const muon_mxfp4* b, const vo
   std::memset(&p, 0, sizeof(p));
   const muon_mxfp4* l = pl.swap ? b : a;
   const muon_mxfp4* r = pl.swap ? a : b;
-  if ((st = operand_maps(l, 128, 1, &p.rows_l, &p.scales_l)) != MUON_OK) return st;
-  if ((st = operand_maps(r, pl.few ? pl.nt : 128, pl.few ? 1 : 2, &p.rows_r, &p.scales_r)) != MUON_OK) return st;
+  if ((st = operand_maps(l, 128, pl.few ? 0 : 1, &p.rows_l, &p.scales_l)) != MUON_OK) return st;
+  if ((st = operand_maps(r, pl.few ? pl.nt : 128, pl.few ? 0 : 2, &p.rows_r, &p.scales_r)) != MUON_OK) return st;
   // whole chunks are stored by TMA where out's rows start on 16-byte boundaries
   p.tma_out = !pl.few && pl.split == 1 && !add && s.n * dtype_size(out_dtype) % 16 == 0 ? 1 : 0;
   if (p.tma_out) {

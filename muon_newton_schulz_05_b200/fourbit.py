@@ -46,17 +46,29 @@ class Mxfp4Linear:
         self.ws_y = mb.alloc_matmul_workspace(*max(sizes, key=lambda s: mb.matmul_workspace_size(*s)), device)
         self.ws_dx = mb.alloc_matmul_workspace(self.dy.shape, self.w_t.shape, device)
         self.ws_dw = mb.alloc_matmul_workspace(self.dy_t.shape, self.x_t.shape, device)
+        self._has_w = self._has_x = False   # `refresh` and `forward` have been called
 
     def _check(self, t, shape: Tuple[int, int, int], name: str) -> None:
         s = tuple(t.shape)
         if s != shape and (shape[0] != 1 or s != shape[1:]):
             raise ValueError(f"{name} must be {list(shape)}, not {list(s)}")
 
-    def refresh(self, param) -> None:
+    def refresh(self, param, ema=None, w_final: float = 0.35) -> None:
         """Quantises the parameters (bf16 or fp32 [count, rows, cols]) for the
-        passes that follow; call it after every step that changes them."""
+        passes that follow; call it after every step that changes them. With
+        ema (fp32) the layer gets the readout blend w_final param + (1 - w_final)
+        ema instead, which is not stored."""
         self._check(param, self.shape, "param")
-        mb.mxfp4_quantize(param, self.w, self.w_t)
+        if ema is None:
+            mb.mxfp4_quantize(param, self.w, self.w_t)
+        else:
+            self._check(ema, self.shape, "ema")
+            mb.mxfp4_readout(param, ema, self.w, self.w_t, w_final=w_final)
+        self._has_w = True
+
+    def _need_weights(self) -> None:
+        if not self._has_w:
+            raise RuntimeError("call refresh(param) before the first pass")
 
     def forward(self, x, out, rng=None) -> None:
         """out [count, tokens, rows] = dropout(x) W^T; x [count, tokens, cols].
@@ -64,7 +76,9 @@ class Mxfp4Linear:
         count, rows, cols = self.shape
         self._check(x, (count, self.tokens, cols), "x")
         self._check(out, (count, self.tokens, rows), "out")
+        self._need_weights()
         mb.mxfp4_quantize(x, self.x, self.x_t, dropout=self.p, rng=rng if self.p > 0 else None, site=self.site)
+        self._has_x = True
         mb.mxfp4_matmul(self.x, self.w, out, self.ws_y)
 
     def infer(self, x, out) -> None:
@@ -77,6 +91,7 @@ class Mxfp4Linear:
             raise ValueError(f"x must have 1 to {self.tokens} tokens")
         self._check(x, (count, tokens, cols), "x")
         self._check(out, (count, tokens, rows), "out")
+        self._need_weights()
         q = self._first_tokens(tokens)
         mb.mxfp4_quantize(x, q)
         mb.mxfp4_matmul(q, self.w, out, self.ws_y)
@@ -101,6 +116,9 @@ class Mxfp4Linear:
             self._check(dx, (count, self.tokens, cols), "dx")
         if rng is None:
             raise ValueError("backward needs rng")
+        self._need_weights()
+        if not self._has_x:
+            raise RuntimeError("backward needs a forward pass")
         mb.mxfp4_quantize(dy, self.dy if dx is not None else None, self.dy_t, stochastic=True, rng=rng, site=self.site)
         mb.mxfp4_matmul(self.dy_t, self.x_t, grad, self.ws_dw, add=grad if accumulate else None)
         if dx is not None:

@@ -149,6 +149,60 @@ def test_infer_one_token_between_the_passes(mb):
     assert torch.equal(grads[0][0], grads[1][0]) and torch.equal(grads[0][1], grads[1][1])
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_averaged_weights(mb, dtype):
+    """refresh with an average gives the layer the blend: the codes of
+    readout_blend's fp32 result, in both orientations."""
+    from muon_newton_schulz_05_b200.fourbit import Mxfp4Linear
+    shape = (2, 130, 96)
+    g = torch.Generator().manual_seed(12)
+    w = torch.randn(shape, generator=g).to(dtype).cuda()
+    ema, blend = torch.randn(shape, generator=g).cuda(), torch.empty(shape, device="cuda")
+    mb.readout_blend(w, ema, blend, w_final=0.25)
+    a, b = Mxfp4Linear(shape, 3), Mxfp4Linear(shape, 3)
+    a.refresh(w, ema, w_final=0.25)
+    b.refresh(blend)
+    for q, r in ((a.w, b.w), (a.w_t, b.w_t)):
+        assert torch.equal(q.data, r.data) and torch.equal(q.scales, r.scales)
+    x = torch.randn((2, 3, 96), generator=g).cuda()
+    ya, yb = torch.empty(2, 3, 130, device="cuda"), torch.empty(2, 3, 130, device="cuda")
+    a.infer(x, ya)
+    b.infer(x, yb)
+    assert torch.equal(ya, yb)
+
+
+def test_first_calls_of_a_process_can_be_captured():
+    """Nothing has to run before a capture: the library's first call of each
+    kind in a process is one inside it, and the replay gives the eager result."""
+    import subprocess
+    import sys
+    code = """
+import torch, muon_newton_schulz_05_b200 as mb
+from muon_newton_schulz_05_b200.fourbit import Mxfp4Linear
+lin = Mxfp4Linear((1, 96, 160), 200, p=0.25)
+w, x, dy = torch.randn(1, 96, 160, device="cuda"), torch.randn(1, 200, 160, device="cuda"), torch.randn(1, 200, 96, device="cuda")
+y, grad, dx, back = (torch.zeros_like(t) for t in (dy, w, x, w))
+rng = torch.tensor([1, 2], device="cuda")
+def step():
+    lin.refresh(w)
+    lin.forward(x, y, rng)
+    lin.backward(dy, grad, dx, rng)
+    mb.mxfp4_dequantize(lin.w, back)
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    step()
+graph.replay()
+got = [t.clone() for t in (y, grad, dx, back)]
+step()
+assert lin.device_status() == 0
+assert all(torch.equal(a, b) and bool(a.any()) for a, b in zip(got, (y, grad, dx, back)))
+"""
+    import os
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
+
+
 def _training(mb, seed=0):
     """Two layers with dropout between them, a bank per layer, Muon on both."""
     from muon_newton_schulz_05_b200.fourbit import Mxfp4Linear

@@ -204,3 +204,14 @@ def test_linear_layer_refusals():
     lin = Mxfp4Linear((1, 256, 16384), tokens=20480, device="cpu")
     for tokens in (1, 64, 65, 256, 257, 1000, 20480):
         assert lin.ws_y.numel() >= mb.matmul_workspace_size((1, tokens, 16384), lin.w.shape)
+
+
+def test_linear_layer_refuses_passes_out_of_order():
+    from muon_newton_schulz_05_b200.fourbit import Mxfp4Linear
+    lin = Mxfp4Linear((2, 24, 40), tokens=7, device="cpu")
+    x, y, w, rng = torch.zeros(2, 7, 40), torch.zeros(2, 7, 24), torch.zeros(2, 24, 40), torch.zeros(2, dtype=torch.int64)
+    for f in (lambda: lin.forward(x, y), lambda: lin.infer(x[:, :1], y[:, :1]), lambda: lin.backward(y, w, rng=rng)):
+        with pytest.raises(RuntimeError, match="refresh"):
+            f()
+    with pytest.raises(ValueError):
+        lin.refresh(w, ema=x)
