@@ -84,7 +84,8 @@ class Mxfp4Linear:
     def infer(self, x, out) -> None:
         """out = x W^T without dropout; any number of tokens up to the layer's,
         in particular one. Leaves what the last forward pass kept for its
-        backward pass."""
+        backward pass. It uses the forward pass's workspace, so the two must not
+        overlap on the device, nor two calls of it."""
         count, rows, cols = self.shape
         tokens = x.shape[-2]
         if not 1 <= tokens <= self.tokens:
