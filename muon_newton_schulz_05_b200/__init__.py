@@ -293,14 +293,20 @@ def readout_blend(theta, ema, out, w_final: float = 0.35, stream=None) -> None:
 # ------------------------------------------------------- dropout and 4 bits
 # These calls are short (a few microseconds on the device), so their host side
 # is kept short too: no per-call imports, one pass over the tensors.
-_torch = None
+_torch = _u8 = None
+_codes = {}
 
 
 def _need_torch() -> None:
-    global _torch
+    global _torch, _u8, _codes
     if _torch is None:
         import torch
-        _torch = torch
+        _torch, _u8, _codes = torch, torch.uint8, {torch.float32: F32, torch.bfloat16: BF16}
+
+
+def _code(t) -> int:
+    """_dtype_code after _need_torch()."""
+    return _codes.get(t.dtype, 99)
 
 
 class Mxfp4:
@@ -360,19 +366,20 @@ def _cmx(q: Optional[Mxfp4], what: str):
     if q is None:
         return None
     d, s, c = q.data, q.scales, q._c
-    if d.dtype is not _torch.uint8 or s.dtype is not _torch.uint8:
+    if d.dtype is not _u8 or s.dtype is not _u8:
         raise ValueError(f"{what}: data and scales must be uint8")
-    n = q._bytes[0]
-    if n and (d.numel() != n or s.numel() != q._bytes[1]):
-        raise ValueError(f"{what}: storage of {d.numel()} + {s.numel()} bytes for {n} + {q._bytes[1]}")
-    c.data, c.scales = _ptr(d), _ptr(s)
+    n, m = q._bytes
+    if n and (d.numel() != n or s.numel() != m):
+        raise ValueError(f"{what}: storage of {d.numel()} + {s.numel()} bytes for {n} + {m}")
+    if not d.is_contiguous() or not s.is_contiguous():
+        raise ValueError("tensors passed to the library must be contiguous")
+    c.data, c.scales = d.data_ptr(), s.data_ptr()
     return q._ref
 
 
 def _launch(stream, fn, what, x, others, *args) -> None:
     """fn(*args, stream) with the device of the call's tensors current, on the
     given stream or that device's current one."""
-    _need_torch()
     dev = x.get_device()
     for t in others:
         if t is not None and t.get_device() != dev:
@@ -404,6 +411,7 @@ def dropout(x, out, p: float, rng, site: int = 0, residual=None, stream=None) ->
     device, site: the call's place within the step. The mask depends on them,
     the row and the column only; the gradient's pass is the same call on the
     output's gradient."""
+    _need_torch()
     shape = x.shape
     if out.shape != shape or out.dtype != x.dtype:
         raise ValueError("out must have x's shape and dtype")
@@ -413,7 +421,7 @@ def dropout(x, out, p: float, rng, site: int = 0, residual=None, stream=None) ->
     cols = shape[-1] if len(shape) else 1
     rows = x.numel() // cols if cols else 0
     _launch(stream, _lib.muon_dropout, "dropout", x, (out, rng, residual), _ptr(x), _ptr(residual), _ptr(out),
-            _dtype_code(x), rows, cols, p, r, site)
+            _code(x), rows, cols, p, r, site)
 
 
 def mxfp4_quantize(x, out: Optional[Mxfp4] = None, out_t: Optional[Mxfp4] = None, dropout: float = 0.0,
@@ -424,10 +432,11 @@ def mxfp4_quantize(x, out: Optional[Mxfp4] = None, out_t: Optional[Mxfp4] = None
     same rng and site, x seen as [count * rows, cols]); stochastic rounds
     without bias, out and out_t independently. A block with an infinity or a
     NaN stands for NaN."""
+    _need_torch()
     c, r, k = _shape3(x.shape)
     q, qt, g = _cmx(out, "out"), _cmx(out_t, "out_t"), _rng_ptr(rng)
     _launch(stream, _lib.muon_mxfp4_quantize, "mxfp4_quantize", x, (rng, *_storage(out), *_storage(out_t)),
-            _ptr(x), _dtype_code(x), c, r, k, q, qt, dropout, 1 if stochastic else 0, g, site)
+            _ptr(x), _code(x), c, r, k, q, qt, dropout, 1 if stochastic else 0, g, site)
 
 
 def _storage(q: Optional[Mxfp4]):
@@ -438,12 +447,13 @@ def mxfp4_readout(theta, ema, out: Optional[Mxfp4] = None, out_t: Optional[Mxfp4
                   w_final: float = 0.35, stream=None) -> None:
     """Quantises the readout blend w_final theta + (1 - w_final) ema without
     storing it: the codes of readout_blend's fp32 result."""
-    if ema.shape != theta.shape or _dtype_code(ema) != F32:
+    _need_torch()
+    if ema.shape != theta.shape or _code(ema) != F32:
         raise ValueError("ema must be float32 of theta's shape")
     c, r, k = _shape3(theta.shape)
     q, qt = _cmx(out, "out"), _cmx(out_t, "out_t")
     _launch(stream, _lib.muon_mxfp4_readout, "mxfp4_readout", theta, (ema, *_storage(out), *_storage(out_t)),
-            _ptr(theta), _dtype_code(theta), _ptr(ema), w_final, c, r, k, q, qt)
+            _ptr(theta), _code(theta), _ptr(ema), w_final, c, r, k, q, qt)
 
 
 def mxfp4_dequantize(q: Mxfp4, out, stream=None) -> None:
@@ -454,7 +464,7 @@ def mxfp4_dequantize(q: Mxfp4, out, stream=None) -> None:
     if shape != q._shape and (q._shape[0] != 1 or shape != q._shape[1:]):
         raise ValueError("out must have q's shape")
     _launch(stream, _lib.muon_mxfp4_dequantize, "mxfp4_dequantize", out, (q.data, q.scales), cq, _ptr(out),
-            _dtype_code(out))
+            _code(out))
 
 
 def matmul_workspace_size(a_shape, b_shape) -> int:
@@ -482,14 +492,14 @@ def mxfp4_matmul(a: Mxfp4, b: Mxfp4, out, workspace, add=None, stream=None) -> N
     reports a device-side wait that ran out."""
     ca, cb = _cmx(a, "a"), _cmx(b, "b")
     (na, m, _), (nb, n, _) = a._shape, b._shape
-    shape, count = tuple(out.shape), na if na > nb else nb
+    shape, count = out.shape, na if na > nb else nb
     if shape != (count, m, n) and (count != 1 or shape != (m, n)):
         raise ValueError("out must be [count, a's rows, b's rows]")
-    if add is not None and (add.shape != out.shape or add.dtype != out.dtype):
+    if add is not None and (add.shape != shape or add.dtype != out.dtype):
         raise ValueError("add must have out's shape and dtype")
     _launch(stream, _lib.muon_mxfp4_matmul, "mxfp4_matmul", out,
-            (a.data, a.scales, b.data, b.scales, workspace, add), ca, cb, _ptr(add), _ptr(out), _dtype_code(out),
-            _ptr(workspace), workspace.numel() * workspace.element_size())
+            (a.data, a.scales, b.data, b.scales, workspace, add), ca, cb, _ptr(add), _ptr(out), _code(out),
+            _ptr(workspace), workspace.nbytes)
 
 
 def device_status(workspace, stream=None, clear: bool = False) -> int:

@@ -66,6 +66,7 @@ struct DequantParams {
 };
 
 cudaError_t launch_dropout(const DropoutParams& p, bool bf16, int sms, cudaStream_t s);
+cudaError_t quantize_prepare();   // kernel attributes; once per device
 cudaError_t launch_quantize(const QuantParams& p, bool bf16, int sms, cudaStream_t s);
 cudaError_t launch_dequantize(const DequantParams& p, bool bf16, int sms, cudaStream_t s);
 

@@ -69,6 +69,33 @@ bool dropout_terms(double p, uint32_t* threshold, float* scale) {
   return true;
 }
 
+// Devices whose kernels have their attributes set.
+struct LowbitDevice {
+  bool quantize = false, gemm = false;
+  int pairs = 0;
+};
+LowbitDevice g_lowbit[64];
+std::mutex g_lowbit_mu;
+
+// The current device, prepared for quantisation or (pairs given) for products.
+muon_status lowbit_device(int* sms, int* pairs = nullptr) {
+  const muon_status st = library_device(sms);
+  if (st != MUON_OK) return st;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return MUON_ERR_CUDA;
+  std::lock_guard<std::mutex> lk(g_lowbit_mu);
+  LowbitDevice& d = g_lowbit[dev];
+  if (pairs) {
+    if (!d.gemm && mx_gemm_prepare(&d.pairs) != cudaSuccess) return MUON_ERR_CUDA;
+    d.gemm = true;
+    *pairs = d.pairs;
+  } else {
+    if (!d.quantize && quantize_prepare() != cudaSuccess) return MUON_ERR_CUDA;
+    d.quantize = true;
+  }
+  return MUON_OK;
+}
+
 muon_status run_quantize(QuantParams& q, int32_t dtype, int64_t count, int64_t rows, int64_t cols,
                          const muon_mxfp4* out, const muon_mxfp4* out_t, void* stream) {
   if (!q.x || (!out && !out_t)) return MUON_ERR_NULL;
@@ -96,7 +123,7 @@ muon_status run_quantize(QuantParams& q, int32_t dtype, int64_t count, int64_t r
     if (overlaps(w[i], {q.rng, 16})) return MUON_ERR_ALIAS;
   }
   int sms = 0;
-  const muon_status st = library_device(&sms);
+  const muon_status st = lowbit_device(&sms);
   if (st != MUON_OK) return st;
   q.q = out ? static_cast<uint8_t*>(out->data) : nullptr;
   q.s = out ? static_cast<uint8_t*>(out->scales) : nullptr;
@@ -117,28 +144,6 @@ muon_status run_quantize(QuantParams& q, int32_t dtype, int64_t count, int64_t r
 }
 
 // ------------------------------------------------------------------- product
-struct GemmDevice {
-  bool ready = false;
-  int pairs = 0;
-};
-GemmDevice g_gemm[64];
-std::mutex g_gemm_mu;
-
-muon_status gemm_device(int* sms, int* pairs) {
-  muon_status st = library_device(sms);
-  if (st != MUON_OK) return st;
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return MUON_ERR_CUDA;
-  std::lock_guard<std::mutex> lk(g_gemm_mu);
-  GemmDevice& d = g_gemm[dev];
-  if (!d.ready) {
-    if (mx_gemm_prepare(&d.pairs) != cudaSuccess) return MUON_ERR_CUDA;
-    d.ready = true;
-  }
-  *pairs = d.pairs;
-  return MUON_OK;
-}
-
 bool gemm_shape_ok(const MxGemmShape& s) {
   return shape_ok(s.count, s.m, s.k) && shape_ok(s.count, s.n, s.k) && shape_ok(s.count, s.m, s.n);
 }
@@ -298,7 +303,7 @@ muon_status muon_mxfp4_matmul(const muon_mxfp4* a, const muon_mxfp4* b, const vo
   if ((add && add != out && overlaps(o, {add, o.n})) || overlaps(o, w) || overlaps(w, {add, o.n}))
     return MUON_ERR_ALIAS;
   int sms = 0, pairs = 0;
-  if ((st = gemm_device(&sms, &pairs)) != MUON_OK) return st;
+  if ((st = lowbit_device(&sms, &pairs)) != MUON_OK) return st;
 
   MxGemmParams p;
   std::memset(&p, 0, sizeof(p));

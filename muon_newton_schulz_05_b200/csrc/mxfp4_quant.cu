@@ -516,31 +516,51 @@ __global__ void __launch_bounds__(QuantConfig<kSrc>::kThreads, QuantConfig<kSrc>
   if (turn > 0) flush_scales(last, turn - 1);
 }
 
+// The kernel of a variant, for its launch and for its preparation.
 template <int kSrc, bool kDrop, bool kStoch>
-static cudaError_t launch_one(const QuantParams& p, int sms, cudaStream_t s) {
+static cudaError_t launch_one(const QuantParams* p, int sms, cudaStream_t s) {
   using C = QuantConfig<kSrc>;
-  const cudaError_t e = cudaFuncSetAttribute(quantize_kernel<kSrc, kDrop, kStoch>,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
-  if (e != cudaSuccess) return e;
-  const int tiles = p.count * p.tiles_r * p.tiles_c, most = C::blocks(kStoch) * sms;
-  quantize_kernel<kSrc, kDrop, kStoch><<<tiles < most ? tiles : most, C::kThreads, C::kSmem, s>>>(p);
+  if (!p)
+    return cudaFuncSetAttribute(quantize_kernel<kSrc, kDrop, kStoch>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                C::kSmem);
+  const int tiles = p->count * p->tiles_r * p->tiles_c, most = C::blocks(kStoch) * sms;
+  quantize_kernel<kSrc, kDrop, kStoch><<<tiles < most ? tiles : most, C::kThreads, C::kSmem, s>>>(*p);
   return cudaGetLastError();
 }
 
 template <int kSrc>
 static cudaError_t launch_src(const QuantParams& p, int sms, cudaStream_t s) {
   if constexpr (QuantConfig<kSrc>::kBlend) {
-    return launch_one<kSrc, false, false>(p, sms, s);
+    return launch_one<kSrc, false, false>(&p, sms, s);
   } else {
     if (p.threshold)
-      return p.stochastic ? launch_one<kSrc, true, true>(p, sms, s) : launch_one<kSrc, true, false>(p, sms, s);
-    return p.stochastic ? launch_one<kSrc, false, true>(p, sms, s) : launch_one<kSrc, false, false>(p, sms, s);
+      return p.stochastic ? launch_one<kSrc, true, true>(&p, sms, s) : launch_one<kSrc, true, false>(&p, sms, s);
+    return p.stochastic ? launch_one<kSrc, false, true>(&p, sms, s) : launch_one<kSrc, false, false>(&p, sms, s);
   }
 }
 
 cudaError_t launch_quantize(const QuantParams& p, bool bf16, int sms, cudaStream_t s) {
   if (p.ema) return bf16 ? launch_src<kSrcBlendBf16>(p, sms, s) : launch_src<kSrcBlendF32>(p, sms, s);
   return bf16 ? launch_src<kSrcBf16>(p, sms, s) : launch_src<kSrcF32>(p, sms, s);
+}
+
+template <int kSrc>
+static cudaError_t prepare_src() {
+  cudaError_t e = launch_one<kSrc, false, false>(nullptr, 0, nullptr);
+  if constexpr (!QuantConfig<kSrc>::kBlend) {
+    if (e == cudaSuccess) e = launch_one<kSrc, false, true>(nullptr, 0, nullptr);
+    if (e == cudaSuccess) e = launch_one<kSrc, true, false>(nullptr, 0, nullptr);
+    if (e == cudaSuccess) e = launch_one<kSrc, true, true>(nullptr, 0, nullptr);
+  }
+  return e;
+}
+
+cudaError_t quantize_prepare() {
+  cudaError_t e = prepare_src<kSrcBf16>();
+  if (e == cudaSuccess) e = prepare_src<kSrcF32>();
+  if (e == cudaSuccess) e = prepare_src<kSrcBlendBf16>();
+  if (e == cudaSuccess) e = prepare_src<kSrcBlendF32>();
+  return e;
 }
 
 // ------------------------------------------------------------------ read-back
