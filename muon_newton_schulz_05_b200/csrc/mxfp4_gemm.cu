@@ -212,6 +212,19 @@ __device__ __forceinline__ void store_chunk(const MxGemmParams& p, uint8_t* buf,
   }
 }
 
+// Brings the addends of a warp's 32 x 128 part of a tile (row per lane) to L2.
+// Loaded from DRAM when the accumulator is there, chunk after chunk, they cost
+// more than the rest of the tile.
+template <bool kBf16>
+__device__ __forceinline__ void prefetch_addends(const MxGemmParams& p, long long base, int row, int col) {
+  constexpr int kLine = kBf16 ? 64 : 32;   // elements in 128 bytes
+  const int end = min(col + 128, p.n);
+  if (row >= p.m || col >= end) return;
+  const long long at = base + static_cast<long long>(row) * p.n;
+  for (int c = col; c < end; c += kLine) prefetch_l2(static_cast<const uint8_t*>(p.add) + (at + c) * (kBf16 ? 2 : 4));
+  prefetch_l2(static_cast<const uint8_t*>(p.add) + (at + end - 1) * (kBf16 ? 2 : 4));
+}
+
 }  // namespace
 
 // ------------------------------------------------------------------ pair kernel
@@ -472,8 +485,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
     uint8_t* buf = chunks + (warp - 2) * kPChunkBytes;
     uint32_t acc = 0, phase = 0;
     bool ok = true;
+    auto prefetch = [&](int t) {
+      const MxTile T = mx_tile(p, t);
+      prefetch_addends<kBf16>(p, T.c * p.stride_c, T.im * kPTile + kRows * static_cast<int>(rank) + 32 * q + lane,
+                              T.in * kPTile + half * 128);
+    };
+    if (kStore == kStoreAdd && pair < ntiles) prefetch(pair);
     for (int t = pair; ok && t < ntiles; t += npairs) {
       const MxTile T = mx_tile(p, t);
+      if (kStore == kStoreAdd && t + npairs < ntiles) prefetch(t + npairs);
       const bool overlapped = (acc == 0) == (half == 1);
       if (!overlapped) {  // this warp holds nothing the next tile's MMAs would overwrite
         tc_fence_before();
@@ -559,10 +579,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
 template <bool kBf16>
 __global__ void __launch_bounds__(256) mx_reduce_kernel(const __grid_constant__ MxGemmParams p) {
   __shared__ float turn[32][33];
-  // launched while the pair kernel still runs: its partial tiles are complete
-  // once this returns
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (*reinterpret_cast<const volatile int*>(p.status) != 0) return;
   const int chunk = static_cast<int>(blockIdx.x & 63u), tile = static_cast<int>(blockIdx.x >> 6);
   const MxTile T = mx_tile(p, tile * p.split);
   const int j = chunk & 3, half = (chunk >> 2) & 1, q = (chunk >> 3) & 3, rank = chunk >> 5;
@@ -578,6 +594,10 @@ __global__ void __launch_bounds__(256) mx_reduce_kernel(const __grid_constant__ 
     for (int i = 0; i < 4; ++i)
       if (col + i < p.n) add[i] = load1t<kBf16>(p.add, at + i);
   }
+  // launched while the pair kernel still runs: its partial tiles are complete
+  // once this returns (the addends are not its work)
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (*reinterpret_cast<const volatile int*>(p.status) != 0) return;
   const float4* src = reinterpret_cast<const float4*>(
       p.part + static_cast<long long>(tile) * p.split * (kPTile * kPTile) + chunk * 1024) + threadIdx.x;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -714,6 +734,15 @@ __global__ void __launch_bounds__(kFewThreads) mx_gemm_few_kernel(const __grid_c
   if (warp == 1) {
     tmem_alloc(&tmem_slot, kFewColumns);
     tmem_relinquish();
+  }
+  if (p.add && warp >= 2) {   // the addends to L2: 32 left rows at a time where those are neighbours in out
+    const int per = p.stride_l == 1 ? 4 : kRows, total = p.stride_l == 1 ? 4 * p.n : kRows;
+    for (int i = static_cast<int>(threadIdx.x) - 64; i < total; i += 128) {
+      const int l = im * kRows + i % per * (kRows / per);
+      if (l < p.m)
+        prefetch_l2(static_cast<const uint8_t*>(p.add) +
+                    (c * p.stride_c + l * p.stride_l + i / per * p.stride_r) * (kBf16 ? 2 : 4));
+    }
   }
   tc_fence_before();
   __syncthreads();
