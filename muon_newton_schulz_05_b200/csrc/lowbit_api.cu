@@ -311,8 +311,8 @@ muon_status muon_mxfp4_matmul(const muon_mxfp4* a, const muon_mxfp4* b, const vo
   const muon_mxfp4* r = pl.swap ? a : b;
   if ((st = operand_maps(l, 128, pl.few ? 0 : 1, &p.rows_l, &p.scales_l)) != MUON_OK) return st;
   if ((st = operand_maps(r, pl.few ? pl.nt : 128, pl.few ? 0 : 2, &p.rows_r, &p.scales_r)) != MUON_OK) return st;
-  // whole chunks are stored by TMA where out's rows start on 16-byte boundaries
-  p.tma_out = !pl.few && pl.split == 1 && !add && s.n * dtype_size(out_dtype) % 16 == 0 ? 1 : 0;
+  // results are stored, and addends loaded, by TMA where out's rows start on 16-byte boundaries
+  p.tma_out = !pl.few && pl.split == 1 && s.n * dtype_size(out_dtype) % 16 == 0 ? 1 : 0;
   if (p.tma_out) {
     const bool bf16 = out_dtype == MUON_BF16;
     const cuuint64_t d[3] = {static_cast<cuuint64_t>(s.n), static_cast<cuuint64_t>(s.m),
@@ -320,9 +320,10 @@ muon_status muon_mxfp4_matmul(const muon_mxfp4* a, const muon_mxfp4* b, const vo
     const cuuint64_t st2[2] = {static_cast<cuuint64_t>(s.n * dtype_size(out_dtype)),
                                static_cast<cuuint64_t>(s.m * s.n * dtype_size(out_dtype))};
     const cuuint32_t box[3] = {bf16 ? 64u : 32u, 32, 1};   // 128-byte rows
-    if ((st = encode_tiled(&p.result, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3,
-                           out, d, st2, box, CU_TENSOR_MAP_SWIZZLE_128B)) != MUON_OK)
-      return st;
+    const CUtensorMapDataType type = bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
+    st = encode_tiled(&p.result, type, 3, out, d, st2, box, CU_TENSOR_MAP_SWIZZLE_128B);
+    if (st == MUON_OK && add) st = encode_tiled(&p.addend, type, 3, add, d, st2, box, CU_TENSOR_MAP_SWIZZLE_128B);
+    if (st != MUON_OK) return st;
   }
   p.add = add;
   p.out = out;

@@ -42,13 +42,14 @@ constexpr int kMxThreads = 96 + 32 * (kMxEpiWarps + kMxScaleWarps);
 
 // pair kernel
 constexpr int kPTile = 256;
-constexpr int kPStages = 5;
+constexpr int kPStages = 5;                        // 4 where the epilogue loads addends by TMA and takes the rest
 constexpr int kPStageBytes = 2 * kCodeBytes;
 constexpr int kSfSlots = 8;                        // the scales' own ring
 constexpr int kPScaleBytes = 3 * kSfGroupBytes;    // A's 128 rows, B's 256
 constexpr int kPChunkBytes = 32 * 128;             // an epilogue warp's buffer: 32 rows of 128 bytes
 constexpr int kPSmemBytes =
     kPStages * kPStageBytes + kSfSlots * kPScaleBytes + kMxEpiWarps * kPChunkBytes + 1024 + 512;
+static_assert(kMxEpiWarps * kPChunkBytes <= kPStageBytes, "a second buffer per epilogue warp in place of a stage");
 constexpr uint32_t kAccOffset = 160;               // first column of the second accumulator
 constexpr int kSfBufs = 4;
 constexpr uint32_t kSfBuf = 24;                    // A: 8 columns, B: 16
@@ -108,6 +109,30 @@ __device__ __forceinline__ void stage_bf16(uint8_t* buf, int lane, const uint32_
   }
 }
 
+// The same results added to the addends that are in the buffer, each lane its
+// own row in place (bf16: two chunks; fp32: one, whose rows are 128 bytes).
+template <bool kBf16>
+__device__ __forceinline__ void add_staged(uint8_t* buf, int lane, const uint32_t* a, int ha, const uint32_t* b) {
+#pragma unroll
+  for (int c = 0; c < (kBf16 ? 2 : 1); ++c) {
+    const uint32_t* r = c ? b : a;
+    const int h = kBf16 ? (c ? 1 - ha : ha) : 0;
+#pragma unroll
+    for (int g = 0; g < (kBf16 ? 4 : 8); ++g) {
+      uint4* at = reinterpret_cast<uint4*>(buf + lane * 128 + (((4 * h + g) ^ (lane & 7)) << 4));
+      const uint4 x = *at;
+      const uint32_t xx[4] = {x.x, x.y, x.z, x.w};
+      uint32_t w[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        w[i] = kBf16 ? pack_bf16x2(__uint_as_float(r[8 * g + 2 * i]) + bf16_lo_f(xx[i]),
+                                   __uint_as_float(r[8 * g + 2 * i + 1]) + bf16_hi_f(xx[i]))
+                     : __float_as_uint(__uint_as_float(r[4 * g + i]) + __uint_as_float(xx[i]));
+      *at = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  }
+}
+
 // The pair of chunks by TMA: one store in bf16, two in fp32 (a chunk's rows are
 // 128 bytes there).
 template <bool kBf16>
@@ -137,11 +162,11 @@ __device__ __forceinline__ void store_pair_tma(const MxGemmParams& p, uint8_t* b
   }
 }
 
-// A chunk for outputs that TMA cannot address, or with an addend: turned in
+// A chunk for outputs that TMA cannot address, perhaps with an addend: turned in
 // shared memory (16-byte group g of row r at g ^ (r & 7)) so that neighbouring
-// lanes load and store neighbouring columns, four at a time where rows have a
-// multiple of 4 elements. The addends of the whole chunk are on their way at
-// once; rows past the end repeat the last one. (For rows that start anywhere,
+// lanes load and store neighbouring columns, four at a time where rows of bf16
+// have a multiple of 4 elements (in fp32 those go by TMA). The addends of 16
+// rows are on their way at once; rows past the end repeat the last one. (For rows that start anywhere,
 // 4-byte stores with a shift by one element, and 16-byte pieces with
 // element-wise ends, both took longer: 21.7 and 24.2 against 18.0 us for
 // 4 x 1000 x 1537 x 771. Such rows cost partial sectors either way; 1536
@@ -157,58 +182,44 @@ __device__ __forceinline__ void store_chunk(const MxGemmParams& p, uint8_t* buf,
   __syncwarp();
   const int rows = min(32, p.m - row);
   if (rows <= 0) return;
-  if (vec) {   // 8 lanes per row, 4 columns each
+  if (kBf16 && vec) {   // 8 lanes per row, 4 columns each
     const int c = col + 4 * (lane & 7);
     if (c >= p.n) return;
     const long long at = base + static_cast<long long>(row) * p.n + c;
-    uint4 add[8];   // four values: fp32, or bf16 in x and y
+    uint2 add[8];
     if (kAdd) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const long long e = at + static_cast<long long>(min(4 * i + (lane >> 3), rows - 1)) * p.n;
-        if (kBf16) {
-          const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(p.add) + e);
-          add[i].x = w.x;
-          add[i].y = w.y;
-        } else {
-          add[i] = *reinterpret_cast<const uint4*>(static_cast<const float*>(p.add) + e);
-        }
-      }
+      for (int i = 0; i < 8; ++i)
+        add[i] = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(p.add) + at +
+                                                 static_cast<long long>(min(4 * i + (lane >> 3), rows - 1)) * p.n);
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int rr = 4 * i + (lane >> 3);
       float4 v = *reinterpret_cast<const float4*>(buf + rr * 128 + (((lane & 7) ^ (rr & 7)) << 4));
-      const long long e = at + static_cast<long long>(rr) * p.n;
-      if (kBf16) {
-        if (kAdd) {
-          v.x += bf16_lo_f(add[i].x); v.y += bf16_hi_f(add[i].x); v.z += bf16_lo_f(add[i].y); v.w += bf16_hi_f(add[i].y);
-        }
-        if (rr < rows)
-          *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + e) =
-              make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
-      } else {
-        if (kAdd) {
-          v.x += __uint_as_float(add[i].x); v.y += __uint_as_float(add[i].y);
-          v.z += __uint_as_float(add[i].z); v.w += __uint_as_float(add[i].w);
-        }
-        if (rr < rows) *reinterpret_cast<float4*>(static_cast<float*>(p.out) + e) = v;
+      if (kAdd) {
+        v.x += bf16_lo_f(add[i].x); v.y += bf16_hi_f(add[i].x); v.z += bf16_lo_f(add[i].y); v.w += bf16_hi_f(add[i].y);
+      }
+      if (rr < rows)
+        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + at + static_cast<long long>(rr) * p.n) =
+            make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+    }
+  } else if (col + lane < p.n) {   // one column per lane, 16 rows at a time (32 do not fit the registers)
+    const long long at = base + static_cast<long long>(row) * p.n + col + lane;
+#pragma unroll 1
+    for (int r0 = 0; r0 < 32; r0 += 16) {
+      float v[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        v[i] = kAdd ? load1t<kBf16>(p.add, at + static_cast<long long>(min(r0 + i, rows - 1)) * p.n) : 0.0f;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const int rr = r0 + i;
+        const float y =
+            *reinterpret_cast<const float*>(buf + rr * 128 + (((lane >> 2) ^ (i & 7)) << 4) + (lane & 3) * 4);
+        if (rr < rows) store1t<kBf16>(p.out, at + static_cast<long long>(rr) * p.n, kAdd ? v[i] + y : y);
       }
     }
-  } else if (col + lane < p.n) {   // one column per lane
-    const long long at = base + static_cast<long long>(row) * p.n + col + lane;
-    float v[32];
-#pragma unroll
-    for (int rr = 0; rr < 32; ++rr)
-      v[rr] = kAdd ? load1t<kBf16>(p.add, at + static_cast<long long>(min(rr, rows - 1)) * p.n) : 0.0f;
-#pragma unroll
-    for (int rr = 0; rr < 32; ++rr) {
-      const float y = *reinterpret_cast<const float*>(buf + rr * 128 + (((lane >> 2) ^ (rr & 7)) << 4) + (lane & 3) * 4);
-      v[rr] = kAdd ? v[rr] + y : y;
-    }
-#pragma unroll
-    for (int rr = 0; rr < 32; ++rr)
-      if (rr < rows) store1t<kBf16>(p.out, at + static_cast<long long>(rr) * p.n, v[rr]);
   }
 }
 
@@ -228,22 +239,26 @@ __device__ __forceinline__ void prefetch_addends(const MxGemmParams& p, long lon
 }  // namespace
 
 // ------------------------------------------------------------------ pair kernel
-// How results leave: partial tiles of a split product, TMA stores, or loads and
-// stores of the epilogue warps (out's rows do not start on 16-byte boundaries,
-// or there is an addend). One kernel each: together they spill registers.
-enum PairStore : int { kStoreParts = 0, kStoreTma = 1, kStorePlain = 2, kStoreAdd = 3 };
+// How results leave: partial tiles of a split product, TMA stores (and addends by
+// TMA loads), or loads and stores of the epilogue warps where out's rows do not
+// start on 16-byte boundaries. One kernel each: together they spill registers.
+enum PairStore : int { kStoreParts = 0, kStoreTma = 1, kStoreTmaAdd = 2, kStorePlain = 3, kStoreAdd = 4 };
 
 template <bool kBf16, int kStore>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
     mx_gemm_pair_kernel(const __grid_constant__ MxGemmParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* slots = smem + kPStages * kPStageBytes;
+  constexpr bool kTmaAdd = kStore == kStoreTmaAdd;
+  constexpr int kStages = kTmaAdd ? kPStages - 1 : kPStages;
+  constexpr int kChunkBytes = kTmaAdd ? 2 * kPChunkBytes : kPChunkBytes;   // per epilogue warp
+  static_assert(kStages >= kSfBufs, "a scale buffer's last use is among the stages in flight");
+  uint8_t* slots = smem + kStages * kPStageBytes;
   uint8_t* chunks = slots + kSfSlots * kPScaleBytes;
   // both CTAs' codes in shared memory and scales in TMEM
-  uint64_t* full = reinterpret_cast<uint64_t*>(chunks + kMxEpiWarps * kPChunkBytes);
-  uint64_t* empty = full + kPStages;
-  uint64_t* sfull = empty + kPStages;     // scales in shared memory, this CTA's
+  uint64_t* full = reinterpret_cast<uint64_t*>(chunks + kMxEpiWarps * kChunkBytes);
+  uint64_t* empty = full + kStages;
+  uint64_t* sfull = empty + kStages;     // scales in shared memory, this CTA's
   uint64_t* sempty = sfull + kSfSlots;
   uint64_t* tfull = sempty + kSfSlots;    // one per accumulator
   // the accumulator of the tile after this one is free; one per accumulator,
@@ -252,7 +267,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
   // waited for it)
   uint64_t* tnext = tfull + 2;
   uint64_t* done = tnext + 2;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
+  uint64_t* addfull = done + 1;           // addends in an epilogue warp's two buffers
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(addfull + 2 * kMxEpiWarps);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -262,7 +278,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
   const int ntiles = p.count * p.tm * p.tn * p.split;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kPStages; ++s) {
+    for (int s = 0; s < kStages; ++s) {
       mbar_init(&full[s], 1 + 2 * kMxScaleWarps);
       mbar_init(&empty[s], 1);
     }
@@ -275,6 +291,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
     mbar_init(&tnext[0], 2 * kMxEpiWarps);
     mbar_init(&tnext[1], 2 * kMxEpiWarps);
     mbar_init(done, 1);
+    for (int s = 0; s < 2 * kMxEpiWarps; ++s) mbar_init(&addfull[s], 1);
     *abort_flag = 0;
     fence_mbar_init();
     tma_prefetch_map(&p.rows_l);
@@ -301,8 +318,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
       const uint32_t full_leader = mapa_shared(smem_u32(full), 0);
       int stage = 0;
       uint32_t phase = 0;
-      int issued[kPStages];
-      for (int s = 0; s < kPStages; ++s) issued[s] = -1;
+      int issued[kStages];
+      for (int s = 0; s < kStages; ++s) issued[s] = -1;
       bool ok = true;
       for (int t = pair; ok && t < ntiles; t += npairs) {
         const MxTile T = mx_tile(p, t);
@@ -321,12 +338,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
           tma_load_3d_pair(st, &p.rows_l, bar, k * kKBytes, lrow, cl);
           tma_load_3d_pair(st + kCodeBytes, &p.rows_r, bar, k * kKBytes, rrow, cr);
           issued[stage] = static_cast<int>(phase);
-          if (++stage == kPStages) { stage = 0; phase ^= 1u; }
+          if (++stage == kStages) { stage = 0; phase ^= 1u; }
         }
       }
       // every load has landed before shared memory is released
       if (rank == 0)
-        for (int s = 0; s < kPStages; ++s)
+        for (int s = 0; s < kStages; ++s)
           if (issued[s] >= 0) drain(&full[s], static_cast<uint32_t>(issued[s]), limit);
     }
   } else if (warp == 1) {
@@ -370,7 +387,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
           const bool whole = kb + 1 < nkb || tail >= 4;
           a += kStageStep;
           sf = sf == (kSfBufs - 1) * kSfBuf ? 0u : sf + kSfBuf;
-          if (++stage == kPStages) { stage = 0; phase ^= 1u; a = desc0; }
+          if (++stage == kStages) { stage = 0; phase ^= 1u; a = desc0; }
           const bool next = mbar_test(full0 + 8u * stage, phase);
           if (whole) {
             if (issuer) {
@@ -433,7 +450,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
     const uint32_t quad = static_cast<uint32_t>(32 * (warp & 3)) << 16;
     const uint32_t full_leader = mapa_shared(smem_u32(full), 0);
     // stage: the one these scales go with; old_stage: the one used kSfBufs stages before
-    int stage = 0, old_stage = kPStages - kSfBufs, slot = 0;
+    int stage = 0, old_stage = kStages - kSfBufs, slot = 0;
     uint32_t phase = 0, old_phase = 1, uses = 0;
     bool ok = true;
     for (int t = pair; ok && t < ntiles; t += npairs) {
@@ -469,9 +486,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
           mbar_arrive_cluster_cta(full_leader + 8u * static_cast<uint32_t>(stage));
         }
         ++uses;
-        if (++stage == kPStages) stage = 0;
+        if (++stage == kStages) stage = 0;
         if (++slot == kSfSlots) { slot = 0; phase ^= 1u; }
-        if (++old_stage == kPStages) { old_stage = 0; old_phase ^= 1u; }
+        if (++old_stage == kStages) { old_stage = 0; old_phase ^= 1u; }
       }
     }
   } else {
@@ -482,7 +499,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
     const int q = warp & 3, half = (warp - 2) >> 2;
     const uint32_t tnext_leader = mapa_shared(smem_u32(tnext), 0);
     const bool vec = (p.n % 4) == 0;
-    uint8_t* buf = chunks + (warp - 2) * kPChunkBytes;
+    uint8_t* buf = chunks + (warp - 2) * kChunkBytes;
     uint32_t acc = 0, phase = 0;
     bool ok = true;
     auto prefetch = [&](int t) {
@@ -490,10 +507,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
       prefetch_addends<kBf16>(p, T.c * p.stride_c, T.im * kPTile + kRows * static_cast<int>(rank) + 32 * q + lane,
                               T.in * kPTile + half * 128);
     };
-    if (kStore == kStoreAdd && pair < ntiles) prefetch(pair);
+    if ((kStore == kStoreAdd || kTmaAdd) && pair < ntiles) prefetch(pair);
+    // Addends by TMA: a tile's boxes of 32 rows x 128 bytes in the order in
+    // which the results come out of TMEM, one load ahead of the one at work
+    // (into the next tile too), the two buffers taken in turn.
+    constexpr int kBoxes = kBf16 ? 2 : 4;
+    uint64_t* bar = addfull + 2 * (warp - 2);
+    uint32_t loads = 0, used = 0;
+    auto load_addends = [&](const MxTile& T, uint32_t acc, int i) {   // lane 0; the buffer's last store has read it
+      const bool back = half == 1 && acc == 0;
+      const int x = kBf16 ? (back ? 1 - i : i) * 64 : (back ? (i < 2 ? 2 + i : 3 - i) : i) * 32;
+      mbar_arrive_expect_tx(&bar[loads & 1u], kPChunkBytes);
+      tma_load_3d(buf + (loads & 1u) * kPChunkBytes, &p.addend, &bar[loads & 1u], T.in * kPTile + half * 128 + x,
+                  T.im * kPTile + kRows * static_cast<int>(rank) + 32 * q, T.c);
+      ++loads;
+    };
+    if (kTmaAdd && lane == 0 && pair < ntiles) load_addends(mx_tile(p, pair), 0, 0);
     for (int t = pair; ok && t < ntiles; t += npairs) {
       const MxTile T = mx_tile(p, t);
-      if (kStore == kStoreAdd && t + npairs < ntiles) prefetch(t + npairs);
+      if ((kStore == kStoreAdd || kTmaAdd) && t + npairs < ntiles) prefetch(t + npairs);
+      int box = 0;
       const bool overlapped = (acc == 0) == (half == 1);
       if (!overlapped) {  // this warp holds nothing the next tile's MMAs would overwrite
         tc_fence_before();
@@ -522,6 +555,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
             for (int g = 0; g < 8; ++g)
               dst[g * 32 + lane] = make_float4(__uint_as_float(r[4 * g]), __uint_as_float(r[4 * g + 1]),
                                                __uint_as_float(r[4 * g + 2]), __uint_as_float(r[4 * g + 3]));
+          }
+        } else if constexpr (kTmaAdd) {
+#pragma unroll
+          for (int i = 0; i < (kBf16 ? 1 : 2); ++i) {
+            const int x = kBf16 ? col + j * 32 : col + (j + (i ? 1 - ha : ha)) * 32;
+            uint8_t* at = buf + (used & 1u) * kPChunkBytes;
+            ok = ok && __all_sync(0xffffffffu, mbar_wait(&bar[used & 1u], (used >> 1) & 1u, abort_flag, p.status, limit));
+            if (!ok) return;
+            add_staged<kBf16>(at, lane, i ? b : a, ha, b);
+            fence_proxy_async_smem();
+            __syncwarp();
+            ++used;
+            ++box;
+            if (lane == 0) {
+              if (row < p.m && x < p.n) tma_store_3d(&p.result, at, x, row, T.c);
+              bulk_commit();
+              bulk_wait_read<1>();   // the store before this one has read the other buffer
+              if (box < kBoxes) load_addends(T, acc, box);
+              else if (t + npairs < ntiles) load_addends(mx_tile(p, t + npairs), acc ^ 1u, 0);
+            }
           }
         } else if constexpr (kStore == kStoreTma) {
           store_pair_tma<kBf16>(p, buf, lane, a, ha, b, T.c, row, col + j * 32);
@@ -555,7 +608,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
       acc ^= 1u;
       if (acc == 0) phase ^= 1u;
     }
-    if (lane == 0) bulk_wait_all();   // every bulk store of this warp has completed
+    if (lane == 0) {
+      // after a wait that ran out: a load under way lands before shared memory is released
+      if (loads > used) drain(&bar[used & 1u], (used >> 1) & 1u, limit);
+      bulk_wait_all();   // every bulk store of this warp has completed
+    }
     __syncwarp();
   }
 
@@ -962,9 +1019,13 @@ static const void* pair_kernel_store(bool bf16) {
 }
 
 static const void* pair_kernel(bool bf16, int store) {
-  if (store == kStoreParts) return reinterpret_cast<const void*>(&mx_gemm_pair_kernel<false, kStoreParts>);
-  return store == kStoreTma ? pair_kernel_store<kStoreTma>(bf16)
-                            : store == kStorePlain ? pair_kernel_store<kStorePlain>(bf16) : pair_kernel_store<kStoreAdd>(bf16);
+  switch (store) {
+    case kStoreParts: return reinterpret_cast<const void*>(&mx_gemm_pair_kernel<false, kStoreParts>);
+    case kStoreTma: return pair_kernel_store<kStoreTma>(bf16);
+    case kStoreTmaAdd: return pair_kernel_store<kStoreTmaAdd>(bf16);
+    case kStorePlain: return pair_kernel_store<kStorePlain>(bf16);
+    default: return pair_kernel_store<kStoreAdd>(bf16);
+  }
 }
 
 template <int NT>
@@ -1025,7 +1086,7 @@ cudaError_t launch_mx_gemm(const MxGemmParams& p, const MxGemmPlan& plan, bool b
   cfg.gridDim = dim3(2 * pairs, 1, 1);
   cfg.blockDim = dim3(kMxThreads, 1, 1);
   cfg.dynamicSmemBytes = kPSmemBytes;
-  const int store = plan.split > 1 ? kStoreParts : p.tma_out ? kStoreTma : p.add ? kStoreAdd : kStorePlain;
+  const int store = plan.split > 1 ? kStoreParts : p.tma_out ? (p.add ? kStoreTmaAdd : kStoreTma) : p.add ? kStoreAdd : kStorePlain;
   cudaError_t e = cudaLaunchKernelExC(&cfg, pair_kernel(bf16, store), args);
   if (e != cudaSuccess || plan.split == 1) return e;
   cfg.gridDim = dim3(static_cast<unsigned>(tiles) * 64u, 1, 1);

@@ -9,6 +9,7 @@ struct MxGemmParams {
   CUtensorMap rows_l, rows_r;      // codes: uint8 [count][rows][blocks * 16], 128-byte swizzle
   CUtensorMap scales_l, scales_r;  // pair kernel, scale tiles: uint32 [count * tiles][ceil(blocks / 4) * 128]
   CUtensorMap result;              // pair kernel: out [count][m][n], boxes of 32 rows x 128 bytes (if tma_out)
+  CUtensorMap addend;              // add, the same way
   int tma_out;
   const uint8_t *sf_l, *sf_r;      // the scale tiles themselves (few-row kernel)
   int sf_groups;                   // tiles per tile row

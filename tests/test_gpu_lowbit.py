@@ -336,6 +336,32 @@ def test_repeated_products_are_bitwise_right(mb, shape):
     assert mb.device_status(ws) == 0
 
 
+@pytest.mark.parametrize("shape", [(1, 4096, 4096, 1792), (5, 1000, 776, 300), (3, 600, 516, 64), (2, 300, 1001, 700)], ids=str)
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_repeated_products_with_an_addend(mb, shape, dtype):
+    """Addends of their own and in place, many times over; ones and minus ones,
+    so that every sum is exact in fp32."""
+    c, m, n, k = shape
+    g = torch.Generator(device="cuda").manual_seed(11)
+    a, b = (torch.randint(0, 2, (c, r, k), generator=g, device="cuda").mul_(2).sub_(1).float() for r in (m, n))
+    qa, qb = mb.alloc_mxfp4((c, m, k)), mb.alloc_mxfp4((c, n, k))
+    mb.mxfp4_quantize(a, qa)
+    mb.mxfp4_quantize(b, qb)
+    add = torch.randint(-100, 101, (c, m, n), generator=g, device="cuda").to(dtype)
+    want = ((a.double() @ b.double().transpose(1, 2)) + add.double()).float().to(dtype)
+    ws = mb.alloc_matmul_workspace(qa.shape, qb.shape)
+    out = torch.empty_like(add)
+    for i in range(30):
+        if i % 2:
+            out.copy_(add)
+            mb.mxfp4_matmul(qa, qb, out, ws, add=out)
+        else:
+            out.fill_(float("nan"))
+            mb.mxfp4_matmul(qa, qb, out, ws, add=add)
+        assert torch.equal(out, want), i
+    assert mb.device_status(ws) == 0
+
+
 LONG = [(1, 200, 200, 16384), (1, 64, 768, 20000), (2, 150, 300, 9000), (1, 768, 768, 32768), (1, 1, 300, 40000)]
 
 
