@@ -24,6 +24,8 @@
 //
 // Every wait is bounded (muon::mbar_wait*); a wait that ran out sets the
 // workspace's status word, and what was not computed is not written.
+#include <type_traits>
+
 #include "dtype_io.cuh"
 #include "mxfp4_gemm.cuh"
 #include "ptx_mxf4.cuh"
@@ -204,20 +206,32 @@ __device__ __forceinline__ void store_chunk(const MxGemmParams& p, uint8_t* buf,
         *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + at + static_cast<long long>(rr) * p.n) =
             make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
     }
-  } else if (col + lane < p.n) {   // one column per lane, 16 rows at a time (32 do not fit the registers)
+  } else if (col + lane < p.n) {   // one column per lane
+    using E = std::conditional_t<kBf16, __nv_bfloat16, float>;
     const long long at = base + static_cast<long long>(row) * p.n + col + lane;
+    E* out = static_cast<E*>(p.out) + at;
+    const E* add = static_cast<const E*>(p.add) + at;
+    const uint8_t* src = buf + (lane & 3) * 4;
+    const int g = lane >> 2;
+    if (rows == 32) {   // no test per row; 16 at a time, 32 addends do not fit the registers
 #pragma unroll 1
-    for (int r0 = 0; r0 < 32; r0 += 16) {
-      float v[16];
+      for (int r0 = 0; r0 < 32; r0 += 16, src += 16 * 128) {
+        float v[16];
+        if (kAdd) {
 #pragma unroll
-      for (int i = 0; i < 16; ++i)
-        v[i] = kAdd ? load1t<kBf16>(p.add, at + static_cast<long long>(min(r0 + i, rows - 1)) * p.n) : 0.0f;
+          for (int i = 0; i < 16; ++i, add += p.n) v[i] = load1t<kBf16>(add, 0);
+        }
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const int rr = r0 + i;
-        const float y =
-            *reinterpret_cast<const float*>(buf + rr * 128 + (((lane >> 2) ^ (i & 7)) << 4) + (lane & 3) * 4);
-        if (rr < rows) store1t<kBf16>(p.out, at + static_cast<long long>(rr) * p.n, kAdd ? v[i] + y : y);
+        for (int i = 0; i < 16; ++i, out += p.n) {
+          const float y = *reinterpret_cast<const float*>(src + i * 128 + ((g ^ (i & 7)) << 4));
+          store1t<kBf16>(out, 0, kAdd ? v[i] + y : y);
+        }
+      }
+    } else {
+#pragma unroll 1
+      for (int rr = 0; rr < rows; ++rr, out += p.n, add += p.n) {
+        const float y = *reinterpret_cast<const float*>(src + rr * 128 + ((g ^ (rr & 7)) << 4));
+        store1t<kBf16>(out, 0, kAdd ? load1t<kBf16>(add, 0) + y : y);
       }
     }
   }
@@ -248,7 +262,7 @@ template <bool kBf16, int kStore>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
     mx_gemm_pair_kernel(const __grid_constant__ MxGemmParams p) {
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* smem = smem_raw + (-smem_u32(smem_raw) & 1023u);   // 1024-byte aligned, and known to be shared memory
   constexpr bool kTmaAdd = kStore == kStoreTmaAdd;
   constexpr int kStages = kTmaAdd ? kPStages - 1 : kPStages;
   constexpr int kChunkBytes = kTmaAdd ? 2 * kPChunkBytes : kPChunkBytes;   // per epilogue warp
@@ -737,7 +751,7 @@ constexpr uint32_t kFewColumns = 128;
 template <int NT, bool kBf16>
 __global__ void __launch_bounds__(kFewThreads) mx_gemm_few_kernel(const __grid_constant__ MxGemmParams p) {
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* smem = smem_raw + (-smem_u32(smem_raw) & 1023u);   // 1024-byte aligned, and known to be shared memory
   __shared__ uint64_t full[few_ring<NT>()], empty[few_ring<NT>()], sready[few_ring<NT>()], done, parts;
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_word;
