@@ -24,8 +24,15 @@
 // once; the K range of a tile is split over the CTAs of a cluster, which add
 // their partial tiles through distributed shared memory in rank order.
 //
-// Every wait is bounded (muon::mbar_wait*); a wait that ran out sets the
-// workspace's status word, and what was not computed is not written.
+// Every wait for a barrier in shared memory is bounded (muon::mbar_wait*); a
+// wait that ran out sets the workspace's status word, and what was not computed
+// is not written. Two waits have no limit of their own: the cluster barrier,
+// which every CTA comes to after bounded waits only, and the TMEM allocation,
+// which waits while other CTAs of the SM hold the columns. A CTA that holds
+// columns may therefore wait for nothing that another CTA's allocation has to
+// come before: the few-row kernel, several of whose CTAs share an SM (more than
+// the 512 columns serve, where K is short), frees its columns before it waits
+// for its cluster. A pair kernel's CTA has its SM to itself (shared memory).
 #include <type_traits>
 
 #include "dtype_io.cuh"
@@ -886,6 +893,14 @@ __global__ void __launch_bounds__(kFewThreads) mx_gemm_few_kernel(const __grid_c
 
   const int q = warp & 3;
   const uint32_t tlane = tmem_base + (static_cast<uint32_t>(32 * q) << 16);
+  auto free_columns = [&] {   // once every warp has read the accumulator
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+      tc_fence_after();
+      tmem_dealloc(tmem_base, kFewColumns);
+    }
+  };
   if (p.split == 1) {
     if (ok && warp >= 2) {
       const int l = im * kRows + 32 * q + lane;
@@ -905,6 +920,7 @@ __global__ void __launch_bounds__(kFewThreads) mx_gemm_few_kernel(const __grid_c
         }
       }
     }
+    free_columns();
   } else {
     // the part as [right row][128], in the ring's memory (its loads have been
     // consumed)
@@ -920,7 +936,10 @@ __global__ void __launch_bounds__(kFewThreads) mx_gemm_few_kernel(const __grid_c
       }
       fence_proxy_async_smem();
     }
-    __syncthreads();
+    // before the cluster barrier: a CTA of this cluster may still wait for
+    // columns that another cluster's CTA holds, and that one for this CTA's
+    free_columns();
+    __syncwarp();
     cluster_wait();   // every CTA's `parts` is initialised
     if (ok && threadIdx.x < static_cast<unsigned>(p.split)) {
       // thread r sends CTA r the right rows it adds up
@@ -969,12 +988,6 @@ __global__ void __launch_bounds__(kFewThreads) mx_gemm_few_kernel(const __grid_c
     }
     __syncwarp();
     cluster_wait();   // and so has what it sent: its memory may go
-  }
-  tc_fence_before();
-  __syncthreads();
-  if (warp == 1) {
-    tc_fence_after();
-    tmem_dealloc(tmem_base, kFewColumns);
   }
 }
 
