@@ -320,7 +320,9 @@ int64_t muon_chain_plan(const int64_t* shapes, int32_t nbanks, int32_t ns_steps,
  * (default 2 s; values <= 0 restore the default). fault_mode 0 = normal;
  * 1 = the Newton-Schulz kernel's producer withholds the first operand stage of
  * block 0's first tile, so the consumer's bounded wait runs out and the call
- * reports MUON_ERR_TIMEOUT through muon_device_status (results invalid). */
+ * reports MUON_ERR_TIMEOUT through muon_device_status (results invalid).
+ * muon_mxfp4_matmul: in modes 1 and 2 some of the threads that load operands
+ * stop before their first or their eighth stage, with the same effect. */
 muon_status muon_set_debug(int32_t fault_mode, double wait_limit_seconds);
 
 #ifdef __cplusplus

@@ -68,6 +68,8 @@ muon_status library_device(int* sms) { return device_state(sms); }
 
 double wait_limit_seconds() { return g_debug.wait_limit_s > 0 ? g_debug.wait_limit_s : 2.0; }
 
+int fault_mode() { return g_debug.fault; }
+
 muon_status encode_tiled(CUtensorMap* m, CUtensorMapDataType type, int rank, const void* ptr,
                          const cuuint64_t* dims, const cuuint64_t* strides, const cuuint32_t* box,
                          CUtensorMapSwizzle swz) {
@@ -679,7 +681,7 @@ int64_t muon_chain_plan(const int64_t* shapes, int32_t nbanks, int32_t ns_steps,
 }
 
 muon_status muon_set_debug(int32_t fault_mode, double wait_limit_seconds) {
-  if (fault_mode < 0 || fault_mode > 1) return MUON_ERR_HPARAM;
+  if (fault_mode < 0 || fault_mode > 2) return MUON_ERR_HPARAM;
   std::lock_guard<std::mutex> lk(g_mu);
   g_debug.fault = fault_mode;
   g_debug.wait_limit_s = wait_limit_seconds > 0 ? wait_limit_seconds : 2.0;

@@ -71,9 +71,11 @@ cudaError_t launch_quantize(const QuantParams& p, bool bf16, int sms, cudaStream
 cudaError_t launch_dequantize(const DequantParams& p, bool bf16, int sms, cudaStream_t s);
 
 // From api.cu: the current device's SM count, the tensor-map encoder (after
-// library_device has succeeded once) and the limit of device-side waits.
+// library_device has succeeded once), the limit of device-side waits and the
+// fault mode (muon_set_debug).
 muon_status library_device(int* sms);
 double wait_limit_seconds();
+int fault_mode();
 muon_status encode_tiled(CUtensorMap* m, CUtensorMapDataType type, int rank, const void* ptr,
                          const cuuint64_t* dims, const cuuint64_t* strides, const cuuint32_t* box,
                          CUtensorMapSwizzle swz);

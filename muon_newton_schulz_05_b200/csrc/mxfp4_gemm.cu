@@ -69,13 +69,27 @@ constexpr int kOverlapChunks = 3;                  // 32-column chunks that the 
 static_assert(kAccOffset + kPTile <= kSfColumn, "the second accumulator ends below the scales");
 static_assert(kPTile - kAccOffset <= kOverlapChunks * 32, "the shared columns are drained first");
 
-__device__ __forceinline__ void drain(uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
+// Waits for what is in flight (copies, MMAs) and certain to come, before the
+// memory it goes to is given up. A bound of its own: the limit of the other
+// waits is the user's and may be what has just run out.
+constexpr uint64_t kDrainNs = 10000000000ull;
+
+__device__ __forceinline__ void drain(uint64_t* bar, uint32_t parity) {
   const uint32_t addr = smem_u32(bar);
+  if (mbar_try_wait(addr, parity)) return;
   const uint64_t t0 = global_timer_ns();
   while (!mbar_try_wait(addr, parity)) {
-    if (global_timer_ns() - t0 > limit_ns) return;
+    if (global_timer_ns() - t0 > kDrainNs) return;
   }
 }
+
+// What the roles of a CTA pair did before one of them gave up: stages whose
+// loads the CTA's producer issued, and for which each scale warp arrived.
+struct GaveUp {
+  int issued;
+  int scaled[kMxScaleWarps];
+  int peer;   // the other CTA gave up
+};
 
 struct MxTile {
   int c, im, in, split, kb0, nkb;
@@ -256,6 +270,42 @@ __device__ __forceinline__ void prefetch_addends(const MxGemmParams& p, long lon
   prefetch_l2(static_cast<const uint8_t*>(p.add) + (at + end - 1) * (kBf16 ? 2 : 4));
 }
 
+// Test hook: in fault modes 1 and 2 one loading thread of each of the first four
+// pairs (codes or scales, of either CTA) stops before its first or its eighth
+// stage, so that waits for what it would have loaded run out.
+__device__ __forceinline__ bool withheld(const MxGemmParams& p, bool scales, int issued) {
+  return p.fault != 0 && blockIdx.x < 8 && issued == (p.fault == 1 ? 0 : 7) &&
+         (blockIdx.x & 1u) == ((blockIdx.x >> 1) & 1u) && scales == (blockIdx.x >= 4);
+}
+
+// After a wait of the pair ran out: lets the last use of each stage whose loads
+// either CTA issued complete, and waits for it. The leader's barrier of a stage
+// counts its producer's arrival, the bytes of both CTAs' loads and the scale
+// warps of both; what will not come is put in its place. (An earlier use of the
+// stage has completed: the loads of a use wait for the MMAs of the one before.)
+// Called by one thread of the leader; no other role of the pair is at work.
+template <int kStages>
+__device__ __noinline__ void finish_stages(uint64_t* full, volatile GaveUp* record) {
+  const uint32_t peer = mapa_shared(smem_u32(const_cast<GaveUp*>(record)), 1);
+  const int issued0 = record->issued, issued1 = ld_cluster(peer);
+  for (int s = 0; s < kStages; ++s) {
+    // the last use of stage s among `issued` ones; -1 (or less): none
+    const int u0 = issued0 > s ? issued0 - 1 - (issued0 - 1 - s) % kStages : -1;
+    const int u1 = issued1 > s ? issued1 - 1 - (issued1 - 1 - s) % kStages : -1;
+    const int u = max(u0, u1);
+    if (u < 0) continue;
+    const uint32_t parity = static_cast<uint32_t>(u / kStages) & 1u;
+    if (mbar_test(smem_u32(&full[s]), parity)) continue;
+    if (u0 < u) mbar_arrive_expect_tx(&full[s], 2 * kCodeBytes);   // the other CTA's loads alone
+    if (u1 < u) mbar_complete_tx(&full[s], 2 * kCodeBytes);        // expected, never issued
+    for (int w = 0; w < 2 * kMxScaleWarps; ++w) {
+      const int scaled = w < kMxScaleWarps ? record->scaled[w] : ld_cluster(peer + 4u * (1 + w - kMxScaleWarps));
+      if (scaled <= u) mbar_arrive(&full[s]);
+    }
+    drain(&full[s], parity);
+  }
+}
+
 }  // namespace
 
 // ------------------------------------------------------------------ pair kernel
@@ -290,6 +340,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
   uint64_t* addfull = done + 1;           // addends in an epilogue warp's two buffers
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(addfull + 2 * kMxEpiWarps);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  volatile GaveUp* record = reinterpret_cast<volatile GaveUp*>(tmem_slot + 2);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint64_t limit = p.wait_limit_ns;
@@ -313,6 +364,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
     mbar_init(done, 1);
     for (int s = 0; s < 2 * kMxEpiWarps; ++s) mbar_init(&addfull[s], 1);
     *abort_flag = 0;
+    record->peer = 0;
     fence_mbar_init();
     tma_prefetch_map(&p.rows_l);
     tma_prefetch_map(&p.rows_r);
@@ -336,10 +388,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
     if (lane == 0) {
       // ---------------------------------------------------------- producer
       const uint32_t full_leader = mapa_shared(smem_u32(full), 0);
-      int stage = 0;
+      int stage = 0, issued = 0;
       uint32_t phase = 0;
-      int issued[kStages];
-      for (int s = 0; s < kStages; ++s) issued[s] = -1;
       bool ok = true;
       for (int t = pair; ok && t < ntiles; t += npairs) {
         const MxTile T = mx_tile(p, t);
@@ -347,7 +397,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
         const int lrow = T.im * kPTile + kRows * static_cast<int>(rank);
         const int rrow = T.in * kPTile + kRows * static_cast<int>(rank);
         for (int kb = 0; kb < T.nkb; ++kb) {
-          if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag, p.status, limit)) {
+          if (withheld(p, false, issued) || !mbar_wait(&empty[stage], phase ^ 1u, abort_flag, p.status, limit)) {
             ok = false;
             break;
           }
@@ -357,14 +407,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
           if (rank == 0) mbar_arrive_expect_tx(&full[stage], 4 * kCodeBytes);
           tma_load_3d_pair(st, &p.rows_l, bar, k * kKBytes, lrow, cl);
           tma_load_3d_pair(st + kCodeBytes, &p.rows_r, bar, k * kKBytes, rrow, cr);
-          issued[stage] = static_cast<int>(phase);
+          ++issued;
           if (++stage == kStages) { stage = 0; phase ^= 1u; }
         }
       }
-      // every load has landed before shared memory is released
-      if (rank == 0)
-        for (int s = 0; s < kStages; ++s)
-          if (issued[s] >= 0) drain(&full[s], static_cast<uint32_t>(issued[s]), limit);
+      record->issued = issued;
     }
   } else if (warp == 1) {
     if (rank == 0) {
@@ -431,24 +478,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
         ++tile;
       }
       if (issuer) umma_commit_pair(done);
-      __syncwarp();
     }
-    if (lane == 0) drain(done, 0, limit);
     __syncwarp();
   } else if (warp == 2 + kMxEpiWarps + kMxScaleWarps) {
     if (lane == 0) {
       // ---------------------------------------------------- scale producer
-      int slot = 0;
+      int slot = 0, issued = 0;
       uint32_t phase = 0;
-      int issued[kSfSlots];
-      for (int s = 0; s < kSfSlots; ++s) issued[s] = -1;
       bool ok = true;
       for (int t = pair; ok && t < ntiles; t += npairs) {
         const MxTile T = mx_tile(p, t);
         const int ltile = (p.share_l ? 0 : T.c) * p.tiles_l + 2 * T.im + static_cast<int>(rank);
         const int rtile = (p.share_r ? 0 : T.c) * p.tiles_r + 2 * T.in;
         for (int kb = 0; kb < T.nkb; ++kb) {
-          if (!mbar_wait(&sempty[slot], phase ^ 1u, abort_flag, p.status, limit)) {
+          if (withheld(p, true, issued) || !mbar_wait(&sempty[slot], phase ^ 1u, abort_flag, p.status, limit)) {
             ok = false;
             break;
           }
@@ -456,12 +499,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
           mbar_arrive_expect_tx(&sfull[slot], kPScaleBytes);
           tma_load_2d(at, &p.scales_l, &sfull[slot], (T.kb0 + kb) * 256, ltile);
           tma_load_2d(at + kSfGroupBytes, &p.scales_r, &sfull[slot], (T.kb0 + kb) * 256, rtile);
-          issued[slot] = static_cast<int>(phase);
+          ++issued;
           if (++slot == kSfSlots) { slot = 0; phase ^= 1u; }
         }
       }
-      for (int s = 0; s < kSfSlots; ++s)
-        if (issued[s] >= 0) drain(&sfull[s], static_cast<uint32_t>(issued[s]), limit);
+      // every load has landed before shared memory is released
+      for (int u = max(0, issued - kSfSlots); u < issued; ++u)
+        drain(&sfull[u % kSfSlots], static_cast<uint32_t>(u / kSfSlots) & 1u);
     }
   } else if (warp >= 2 + kMxEpiWarps) {
     // ------------------------------------------------------ scales to TMEM
@@ -511,6 +555,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
         if (++old_stage == kStages) { old_stage = 0; old_phase ^= 1u; }
       }
     }
+    if (lane == 0) record->scaled[warp & 3] = static_cast<int>(uses);
+    __syncwarp();
   } else {
     // ------------------------------------------------------------ epilogue
     // warp w reads TMEM lanes 32 (w % 4) ..; warps 2..5 the accumulator's
@@ -630,7 +676,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
     }
     if (lane == 0) {
       // after a wait that ran out: a load under way lands before shared memory is released
-      if (loads > used) drain(&bar[used & 1u], (used >> 1) & 1u, limit);
+      if (loads > used) drain(&bar[used & 1u], (used >> 1) & 1u);
       bulk_wait_all();   // every bulk store of this warp has completed
     }
     __syncwarp();
@@ -640,8 +686,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
   if (kStore == kStoreParts) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   tc_fence_before();
   __syncthreads();
-  cluster_arrive_relaxed();   // no MMA of the pair and no remote signal is still in flight
+  // Where every wait of the pair has succeeded, every load has been used, no
+  // MMA is in flight, and the CTAs may part. Where one ran out, both hear of it
+  // here, and stay until the loads of either have landed.
+  const bool gave_up = *abort_flag != 0;
+  if (!gave_up && threadIdx.x == 0) drain(done, 0);
+  __syncwarp();
+  if (gave_up) {
+    if (threadIdx.x == 0) st_cluster(mapa_shared(smem_u32(const_cast<int*>(&record->peer)), rank ^ 1u), 1);
+    __syncwarp();
+    cluster_arrive();
+  } else {
+    cluster_arrive_relaxed();
+  }
   cluster_wait();
+  if (gave_up || record->peer != 0) {
+    cluster_sync();   // both CTAs' records are complete and visible, and `done` is committed
+    if (threadIdx.x == 0) {
+      if (rank == 0) finish_stages<kStages>(full, record);
+      drain(done, 0);
+    }
+    __syncwarp();
+    cluster_sync();
+  }
   if (warp == 1) {
     __syncwarp();
     tc_fence_after();
@@ -838,7 +905,7 @@ __global__ void __launch_bounds__(kFewThreads) mx_gemm_few_kernel(const __grid_c
       }
       // every load has landed before shared memory is released
       for (int kb = sent > p.ring ? sent - p.ring : 0; kb < sent; ++kb)
-        drain(&full[kb % p.ring], static_cast<uint32_t>(kb / p.ring) & 1u, limit);
+        drain(&full[kb % p.ring], static_cast<uint32_t>(kb / p.ring) & 1u);
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -887,7 +954,7 @@ __global__ void __launch_bounds__(kFewThreads) mx_gemm_few_kernel(const __grid_c
     __syncwarp();
   }
   bool ok = mbar_wait(&done, 0, abort_flag, p.status, limit);
-  if (!ok) drain(&done, 0, limit);
+  if (!ok) drain(&done, 0);
   ok = __syncthreads_and(ok && *abort_flag == 0);
   tc_fence_after();
 

@@ -30,6 +30,7 @@ struct MxGemmParams {
   long long stride_l, stride_r, stride_c;  // of out, per left row, right row and matrix
   int* status;
   unsigned long long wait_limit_ns;
+  int fault;                       // test hook (muon_set_debug)
 };
 
 struct MxGemmShape {

@@ -136,8 +136,31 @@ __device__ __forceinline__ void bulk_copy_cluster(uint32_t dst, const void* src,
       : "memory");
 }
 
-// The two halves of a cluster barrier (every thread of the cluster's CTAs).
-// The arrival orders nothing but what a fence before it did.
+// Counts bytes on an mbarrier of this CTA that no copy will bring.
+__device__ __forceinline__ void mbar_complete_tx(uint64_t* bar, uint32_t bytes) {
+  asm volatile("mbarrier.complete_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes)
+               : "memory");
+}
+
+// A word of another CTA's shared memory (shared::cluster address).
+__device__ __forceinline__ void st_cluster(uint32_t addr, int v) {
+  asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+
+__device__ __forceinline__ int ld_cluster(uint32_t addr) {
+  int v;
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+// The halves of a cluster barrier (every thread of the cluster's CTAs). The
+// relaxed arrival orders nothing but what a fence before it did; the other one
+// makes what the thread did before, also in other CTAs' shared memory, visible
+// behind the wait.
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+
 __device__ __forceinline__ void cluster_arrive_relaxed() {
   asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
 }

@@ -1,0 +1,63 @@
+"""4-bit products whose bounded waits run out: a test hook lets some of the
+threads that load operands stop early, and a short limit ends the waits for
+what they would have brought. The kernel records it in the workspace's status
+word and ends in order: what it wrote is right, the rest is as it was, and what
+follows on the same device is right again."""
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+TIMEOUT = 8
+
+
+@pytest.fixture(scope="module")
+def mb():
+    import muon_newton_schulz_05_b200 as m
+    torch.cuda.set_device(0)
+    return m
+
+
+def _ones(mb, rows, k, gen):
+    """+1 and -1, which 4 bits hold exactly, quantised; sums of up to 2^24 of their products are exact in fp32."""
+    x = torch.randint(0, 2, (rows, k), generator=gen, device="cuda").mul_(2).sub_(1).float()
+    q = mb.alloc_mxfp4((rows, k))
+    mb.mxfp4_quantize(x, q)
+    return q, x.double()
+
+
+def _give_up(mb, m, n, k, dtype, add, modes, split):
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    (qa, a), (qb, b) = _ones(mb, m, k, gen), _ones(mb, n, k, gen)
+    ws = mb.alloc_matmul_workspace(qa.shape, qb.shape)
+    assert (ws.numel() > 4096) == split
+    addend = torch.randint(-8, 9, (m, n), generator=gen, device="cuda").to(dtype) if add else None
+    want = a @ b.T
+    want = (want + addend.double() if add else want).float().to(dtype)
+    out = torch.empty(m, n, dtype=dtype, device="cuda")
+    left = torch.full_like(out, 12345.0)
+    for mode in modes * 2:
+        out.copy_(left)
+        mb.set_debug(mode, 0.02)
+        try:
+            mb.mxfp4_matmul(qa, qb, out, ws, add=addend)
+        finally:
+            mb.set_debug(0, 0.0)
+        assert mb.device_status(ws) == TIMEOUT
+        assert bool(((out == want) | (out == left)).all()) and bool((out == left).any())
+        if split:
+            assert torch.equal(out, left)
+            # and so they do, as documented, until the word is cleared
+            mb.mxfp4_matmul(qa, qb, out, ws, add=addend)
+            assert torch.equal(out, left)
+        assert mb.device_status(ws, clear=True) == TIMEOUT and mb.device_status(ws) == 0
+        mb.mxfp4_matmul(qa, qb, out, ws, add=addend)
+        assert torch.equal(out, want) and mb.device_status(ws) == 0
+
+
+# five or four stages in flight, one or many tiles per pair, results by TMA or by the warps, split along k
+@pytest.mark.parametrize("m,n,k,modes,split", [(2600, 2600, 160, [1], False), (1024, 2048, 2560, [1, 2], False),
+                                               (300, 1001, 2200, [1, 2], False), (768, 768, 32768, [1, 2], True)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("add", [False, True])
+def test_large_products_give_up_in_order(mb, m, n, k, dtype, add, modes, split):
+    _give_up(mb, m, n, k, dtype, add, modes, split)
