@@ -828,6 +828,8 @@ __global__ void __launch_bounds__(kFewThreads) mx_gemm_few_kernel(const __grid_c
   __shared__ uint64_t full[few_ring<NT>()], empty[few_ring<NT>()], sready[few_ring<NT>()], done, parts;
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_word;
+  __shared__ int sent;                // this CTA's part is on its way to the others
+  __shared__ volatile int gave_up;    // a CTA of the cluster did
   constexpr int kStage = few_stage_bytes<NT>();
   static_assert(NT + 16 * few_ring<NT>() <= kFewColumns, "accumulator and scales");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -837,6 +839,8 @@ __global__ void __launch_bounds__(kFewThreads) mx_gemm_few_kernel(const __grid_c
   const int tile = static_cast<int>(blockIdx.x) / p.split;
   const int c = tile / p.tm, im = tile - c * p.tm;
   const int kb0 = split * p.kc, nkb = min(p.kc, p.kstages - kb0);
+  // test hook: stages that one CTA (the first or the last of the first cluster) loads
+  const int last = p.fault != 0 && static_cast<int>(blockIdx.x) == (p.fault == 1 ? 0 : p.split - 1) ? nkb - 1 : nkb;
   // split tiles: this CTA adds up the right rows x0 .. x0 + xn - 1
   const int xs = (NT + p.split - 1) / p.split, x0 = split * xs, xn = max(0, min(xs, p.n - x0));
   uint8_t* received = smem + max(p.ring * kStage, NT * kRows * 4);
@@ -868,12 +872,12 @@ __global__ void __launch_bounds__(kFewThreads) mx_gemm_few_kernel(const __grid_c
     }
     mbar_init(&done, 1);
     mbar_init(&parts, 1);
-    abort_word = 0;
+    abort_word = sent = gave_up = 0;
     fence_mbar_init();
     if (p.split > 1) mbar_arrive_expect_tx(&parts, static_cast<uint32_t>(p.split * xn * kRows * 4));
     // the first loads leave before the TMEM allocation and the barrier
 #pragma unroll 1
-    for (int kb = 0; kb < min(p.ring, nkb); ++kb) load(kb, kb);
+    for (int kb = 0; kb < min(p.ring, last); ++kb) load(kb, kb);
   }
   if (warp == 1) {
     tmem_alloc(&tmem_slot, kFewColumns);
@@ -896,15 +900,15 @@ __global__ void __launch_bounds__(kFewThreads) mx_gemm_few_kernel(const __grid_c
 
   if (warp == 0) {
     if (lane == 0) {
-      int stage = 0, sent = min(p.ring, nkb);
+      int stage = 0, issued = min(p.ring, last);
       uint32_t phase = 0;
-      for (int kb = sent; kb < nkb; ++kb, ++sent) {
+      for (int kb = issued; kb < last; ++kb, ++issued) {
         if (!mbar_wait(&empty[stage], phase, abort_flag, p.status, limit)) break;
         load(kb, stage);
         if (++stage == p.ring) { stage = 0; phase ^= 1u; }
       }
       // every load has landed before shared memory is released
-      for (int kb = sent > p.ring ? sent - p.ring : 0; kb < sent; ++kb)
+      for (int kb = max(0, issued - p.ring); kb < issued; ++kb)
         drain(&full[kb % p.ring], static_cast<uint32_t>(kb / p.ring) & 1u);
     }
     __syncwarp();
@@ -1008,6 +1012,7 @@ __global__ void __launch_bounds__(kFewThreads) mx_gemm_few_kernel(const __grid_c
     free_columns();
     __syncwarp();
     cluster_wait();   // every CTA's `parts` is initialised
+    if (ok && threadIdx.x == 0) sent = 1;
     if (ok && threadIdx.x < static_cast<unsigned>(p.split)) {
       // thread r sends CTA r the right rows it adds up
       const int owner = static_cast<int>(threadIdx.x), n = max(0, min(xs, p.n - owner * xs));
@@ -1019,8 +1024,16 @@ __global__ void __launch_bounds__(kFewThreads) mx_gemm_few_kernel(const __grid_c
     // four left rows of a right row per thread; the parts are added in rank
     // order. A part that never came leaves the tile unwritten.
     if (xn > 0) ok = mbar_wait_cluster(&parts, 0, abort_flag, p.status, limit) && ok;
-    __syncwarp();
-    cluster_arrive_relaxed();   // what this CTA was sent has arrived
+    ok = __syncthreads_and(ok);
+    if (ok) {
+      cluster_arrive_relaxed();   // what this CTA was sent has arrived
+    } else {
+      // a part is missing, here or for the others: every CTA has to know
+      if (threadIdx.x < static_cast<unsigned>(p.split))
+        st_cluster(mapa_shared(smem_u32(const_cast<int*>(&gave_up)), threadIdx.x), 1);
+      __syncwarp();
+      cluster_arrive();
+    }
     if (xn > 0) {
       const float4* part = reinterpret_cast<const float4*>(received);
       if (ok) {
@@ -1055,6 +1068,19 @@ __global__ void __launch_bounds__(kFewThreads) mx_gemm_few_kernel(const __grid_c
     }
     __syncwarp();
     cluster_wait();   // and so has what it sent: its memory may go
+    if (gave_up != 0) {
+      // unless a CTA gave up: then parts may be on their way to it still. It
+      // counts those that were never sent itself, and waits for the others.
+      cluster_sync();   // every CTA's `sent` is final and visible
+      if (threadIdx.x == 0 && xn > 0) {
+        int missing = 0;
+        for (int r = 0; r < p.split; ++r) missing += ld_cluster(mapa_shared(smem_u32(&sent), r)) == 0 ? 1 : 0;
+        if (missing > 0) mbar_complete_tx(&parts, static_cast<uint32_t>(missing * xn * kRows * 4));
+        drain(&parts, 0);
+      }
+      __syncwarp();
+      cluster_sync();
+    }
   }
 }
 

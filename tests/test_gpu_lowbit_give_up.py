@@ -61,3 +61,12 @@ def _give_up(mb, m, n, k, dtype, add, modes, split):
 @pytest.mark.parametrize("add", [False, True])
 def test_large_products_give_up_in_order(mb, m, n, k, dtype, add, modes, split):
     _give_up(mb, m, n, k, dtype, add, modes, split)
+
+
+# K whole or split over a cluster, more stages than the ring holds, right rows that some CTAs have none of
+@pytest.mark.parametrize("m,n,k", [(1, 50304, 768), (16, 2560, 2560), (1, 768, 768), (3, 300, 40000), (50, 640, 1024),
+                                   (20, 384, 2048)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("add", [False, True])
+def test_few_row_products_give_up_in_order(mb, m, n, k, dtype, add):
+    _give_up(mb, m, n, k, dtype, add, [1, 2], False)
