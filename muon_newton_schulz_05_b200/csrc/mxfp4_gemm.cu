@@ -412,6 +412,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
         }
       }
       record->issued = issued;
+      // the MMAs' signals for the last stages come from the leader: this CTA
+      // may not leave before they have arrived
+      for (int u = max(0, issued - kStages); ok && u < issued; ++u)
+        ok = mbar_wait(&empty[u % kStages], static_cast<uint32_t>(u / kStages) & 1u, abort_flag, p.status, limit);
     }
   } else if (warp == 1) {
     if (rank == 0) {
@@ -478,6 +482,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
         ++tile;
       }
       if (issuer) umma_commit_pair(done);
+      // the last tile's hand-over signals have arrived too: half of them come
+      // from the other CTA, and nothing else waits for them
+      if (ok) mbar_wait(&tnext[(tile - 1) & 1u], ((tile - 1) >> 1) & 1u, abort_flag, p.status, limit);
     }
     __syncwarp();
   } else if (warp == 2 + kMxEpiWarps + kMxScaleWarps) {

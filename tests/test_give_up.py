@@ -150,3 +150,43 @@ def test_the_plain_rule_leaves_loads_behind():
         pair.land_all()
         stalled += any(pair.full[s].done < n for s, n in waits)
     assert unwatched > 20 and stalled > 50, (unwatched, stalled)
+
+
+def _signals(stages, tiles, per_tile):
+    """Signals that cross between the CTAs of a pair where nothing goes wrong, as (receiver, barrier, completion)."""
+    out = set()
+    for u in range(tiles * per_tile):
+        out |= {(0, "full", u), (1, "empty", u)}          # scale warps of CTA 1; MMA commits of CTA 0
+    for t in range(tiles):
+        out |= {(0, "tnext", t), (1, "tfull", t)}         # epilogue warps of CTA 1; MMA commits
+    return out | {(1, "done", 0)}
+
+
+def _awaited(stages, tiles, per_tile, tails):
+    """Those that some thread of the receiver waits for before it leaves. tails: the producers wait for their
+    last stages to be used, and the MMA warp for the last tile's hand-over."""
+    uses = tiles * per_tile
+    out = {(0, "full", u) for u in range(uses)} | {(1, "tfull", t) for t in range(tiles)} | {(1, "done", 0)}
+    out |= {(1, "empty", u) for u in range(uses if tails else max(0, uses - AHEAD))}   # producer, scale warps
+    return out | {(0, "tnext", t) for t in range(tiles if tails else tiles - 1)}
+
+
+@pytest.mark.parametrize("stages", [4, 5])
+@pytest.mark.parametrize("tiles,per_tile", [(1, 1), (1, 9), (5, 1), (7, 10)])
+def test_no_signal_is_on_its_way_to_a_cta_that_leaves(stages, tiles, per_tile):
+    """The cluster barrier at the kernel's end does not order signals: each is waited for."""
+    assert _signals(stages, tiles, per_tile) <= _awaited(stages, tiles, per_tile, True)
+    assert not _signals(stages, tiles, per_tile) <= _awaited(stages, tiles, per_tile, False)
+
+
+def test_the_kernel_waits_for_its_tails():
+    """The two waits in the source, behind the loops over the tiles."""
+    import os
+    import re
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    src = open(os.path.join(root, "muon_newton_schulz_05_b200", "csrc", "mxfp4_gemm.cu")).read()
+    pair = src[src.index("mx_gemm_pair_kernel(const"):src.index("mx_reduce_kernel(const")]
+    producer = pair[pair.index("record->issued = issued;"):pair.index("MMA issuer")]
+    assert "mbar_wait(&empty[" in producer
+    mma = pair[pair.index("umma_commit_pair(done);"):pair.index("scale producer")]
+    assert re.search(r"if \(ok\) mbar_wait\(&tnext\[\(tile - 1\) & 1u\]", mma)
