@@ -227,7 +227,9 @@ muon_status readout_blend(const void* theta, int32_t theta_dtype, const float* e
  * counter (c >> 3, m * rows + r, lo32(n), (hi32(n) & 0x3fffffff) | d << 30),
  * d = 0 for dropout, 1 for the rounding of out, 2 for the rounding of out_t
  * (whose rows are the source's columns). site tells the calls of one step
- * apart. */
+ * apart. Calls of one seed, domain and offset + site draw the same numbers:
+ * between passes the offset has to move by more than the largest site in use
+ * (after a move by one, site s draws what site s + 1 drew before). */
 typedef struct {
   int64_t count, rows, cols;
   void* data;               /* device, muon_mxfp4_data_size bytes   */

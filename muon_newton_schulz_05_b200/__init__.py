@@ -404,13 +404,25 @@ def _rng_ptr(rng):
     return _ptr(rng)
 
 
+def advance_rng(rng, sites: int) -> None:
+    """Moves rng's offset past the numbers of a forward and backward pass whose
+    calls use the sites 0 .. sites - 1. The numbers of a call depend on
+    offset + site: with a smaller move, a call of the next pass repeats the
+    numbers of another site's call of this one. Enqueued on the current stream
+    (it can be captured)."""
+    _rng_ptr(rng)
+    if isinstance(sites, bool) or not isinstance(sites, int) or sites < 1:
+        raise ValueError("sites must be a positive integer")
+    rng[1] += sites
+
+
 def dropout(x, out, p: float, rng, site: int = 0, residual=None, stream=None) -> None:
     """out = [residual +] dropout(x): elements are dropped with probability p
     (to the nearest 2^-16), the others scaled by 1 / (1 - p). x: [..., cols],
     bf16 or fp32; out may be x or residual. rng: int64 (seed, offset) on the
-    device, site: the call's place within the step. The mask depends on them,
-    the row and the column only; the gradient's pass is the same call on the
-    output's gradient."""
+    device, site: the call's place within the step. The mask depends on the
+    seed, offset + site, the row and the column only (see advance_rng); the
+    gradient's pass is the same call on the output's gradient."""
     _need_torch()
     shape = x.shape
     if out.shape != shape or out.dtype != x.dtype:
@@ -532,7 +544,7 @@ def loaded_library_path() -> str:
 __all__: List[str] = ["Bank", "Hparams", "MuonError", "workspace_size", "alloc_workspace",
                       "muon_step", "anvil_step", "orthogonalize", "ema_update", "readout_blend",
                       "checkpoint_average_betas",
-                      "Mxfp4", "alloc_mxfp4", "mxfp4_storage", "dropout", "mxfp4_quantize", "mxfp4_readout",
+                      "Mxfp4", "alloc_mxfp4", "mxfp4_storage", "advance_rng", "dropout", "mxfp4_quantize", "mxfp4_readout",
                       "mxfp4_dequantize", "mxfp4_matmul", "matmul_workspace_size",
                       "alloc_matmul_workspace", "CMxfp4",
                       "device_status", "set_debug", "set_ns_events", "status_string", "abi_version",

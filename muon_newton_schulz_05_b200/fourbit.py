@@ -11,12 +11,17 @@ and random numbers are formed again from (seed, offset, site).
 
 Every buffer is allocated once, in the constructor; the calls only enqueue
 work on the current stream, so a whole training step (forward, backward, Muon
-step, `refresh`) can be captured in one CUDA graph. Advance the offset in
-`rng` once per step, after the backward pass.
+step, `refresh`) can be captured in one CUDA graph.
+
+Random numbers depend on seed and offset + site. Call `advance(rng, layers)`
+after every backward pass (of each micro-batch, where several are accumulated),
+which moves the offset past all the layers' sites. A smaller step, such as one,
+would give a layer the masks and roundings that its neighbour had the step
+before. Processes that train on different data need seeds of their own.
 """
 from __future__ import annotations
 
-from typing import Tuple
+from typing import Sequence, Tuple
 
 import muon_newton_schulz_05_b200 as mb
 
@@ -26,13 +31,15 @@ class Mxfp4Linear:
     `tokens` rows of input each. Matrices that share their input are one matrix:
     use the bank's view (1, count * rows, cols), of which dx is then one product.
 
-    p: dropout on the input. site: the layer's place in the step (layers of a
-    step need different ones)."""
+    p: dropout on the input. site: the layer's place in the step, from 0 on
+    (layers of a step need different ones)."""
 
     def __init__(self, shape, tokens: int, p: float = 0.0, site: int = 0, device="cuda"):
         count, rows, cols = (int(v) for v in shape)
         if tokens < 1:
             raise ValueError("tokens must be positive")
+        if not 0 <= int(site) < 1 << 62:
+            raise ValueError("site must be from 0 to 2^62 - 1")
         self.shape, self.tokens, self.p, self.site = (count, rows, cols), int(tokens), float(p), int(site)
         new = lambda *s: mb.alloc_mxfp4(s, device)  # noqa: E731
         self.w, self.w_t = new(count, rows, cols), new(count, cols, rows)
@@ -134,3 +141,12 @@ class Mxfp4Linear:
             if code:
                 return code
         return 0
+
+
+def advance(rng, layers: Sequence[Mxfp4Linear]) -> None:
+    """Moves rng's offset past the numbers that a forward and backward pass of
+    these layers used; layers: all that draw from rng."""
+    sites = [lin.site for lin in layers]
+    if len(set(sites)) != len(sites):
+        raise ValueError("layers of a step need different sites")
+    mb.advance_rng(rng, max(sites, default=0) + 1)
