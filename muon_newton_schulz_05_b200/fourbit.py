@@ -134,13 +134,12 @@ class Mxfp4Linear:
             if self.p > 0:
                 mb.dropout(dx, dx, self.p, rng, site=self.site)
 
-    def device_status(self) -> int:
-        """The first error that a product of this layer recorded (it synchronises)."""
-        for ws in (self.ws_y, self.ws_dx, self.ws_dw):
-            code = mb.device_status(ws)
-            if code:
-                return code
-        return 0
+    def device_status(self, clear: bool = False) -> int:
+        """The first error that a product of this layer recorded (it synchronises
+        the current stream). Until it is cleared, products that are split along
+        their contraction leave their outputs as they were."""
+        codes = [mb.device_status(ws, clear=clear) for ws in (self.ws_y, self.ws_dx, self.ws_dw)]
+        return next((code for code in codes if code), 0)
 
 
 def advance(rng, layers: Sequence[Mxfp4Linear]) -> None:

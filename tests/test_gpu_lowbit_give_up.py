@@ -70,3 +70,42 @@ def test_large_products_give_up_in_order(mb, m, n, k, dtype, add, modes, split):
 @pytest.mark.parametrize("add", [False, True])
 def test_few_row_products_give_up_in_order(mb, m, n, k, dtype, add):
     _give_up(mb, m, n, k, dtype, add, [1, 2], False)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_a_set_status_word_holds_split_products_back(mb, dtype):
+    """The word set from the host on a healthy GPU: split products leave out as it was, others do not look."""
+    gen = torch.Generator(device="cuda").manual_seed(6)
+    for m, n, k, split in ((200, 200, 16384, True), (600, 600, 512, False), (5, 600, 4096, False)):
+        (qa, a), (qb, b) = _ones(mb, m, k, gen), _ones(mb, n, k, gen)
+        ws = mb.alloc_matmul_workspace(qa.shape, qb.shape)
+        assert (ws.numel() > 4096) == split
+        want = (a @ b.T).float().to(dtype)
+        out = torch.full((m, n), 12345.0, dtype=dtype, device="cuda")
+        ws[:4] = torch.tensor([TIMEOUT, 0, 0, 0], dtype=torch.uint8, device="cuda")
+        mb.mxfp4_matmul(qa, qb, out, ws)
+        assert torch.equal(out, torch.full_like(out, 12345.0) if split else want)
+        assert mb.device_status(ws, clear=True) == TIMEOUT
+        mb.mxfp4_matmul(qa, qb, out, ws)
+        assert torch.equal(out, want) and mb.device_status(ws) == 0
+
+
+def test_a_layer_reports_and_clears_all_its_products(mb):
+    from muon_newton_schulz_05_b200.fourbit import Mxfp4Linear
+    lin = Mxfp4Linear((1, 200, 320), 16384)
+    gen = torch.Generator(device="cuda").manual_seed(7)
+    w, x, dy = (torch.randn(s, generator=gen, device="cuda") for s in ((1, 200, 320), (16384, 320), (16384, 200)))
+    rng = torch.tensor([1, 0], dtype=torch.int64, device="cuda")
+    y, want, grad = torch.empty_like(dy), torch.empty_like(w), torch.full_like(w, 12345.0)
+    lin.refresh(w)
+    lin.forward(x, y)
+    lin.backward(dy, want, rng=rng)
+    assert lin.device_status() == 0 and lin.ws_dw.numel() > 4096     # the weight gradient is split
+    for ws in (lin.ws_y, lin.ws_dw):
+        ws[0] = TIMEOUT
+    lin.backward(dy, grad, rng=rng)
+    assert bool((grad == 12345.0).all())
+    assert lin.device_status() == TIMEOUT == lin.device_status(clear=True)
+    assert lin.device_status() == 0
+    lin.backward(dy, grad, rng=rng)
+    assert torch.equal(grad, want)
