@@ -515,7 +515,11 @@ def mxfp4_matmul(a: Mxfp4, b: Mxfp4, out, workspace, add=None, stream=None) -> N
 
 
 def device_status(workspace, stream=None, clear: bool = False) -> int:
-    """Synchronises the stream and returns the workspace's device status code."""
+    """Synchronises the stream (default: the current one of the workspace's
+    device) and returns the workspace's device status code."""
+    if stream is None:
+        import torch
+        stream = torch.cuda.current_stream(workspace.device)
     return int(_lib.muon_device_status(_ptr(workspace), workspace.numel() * workspace.element_size(),
                                        _stream_handle(stream), 1 if clear else 0))
 
