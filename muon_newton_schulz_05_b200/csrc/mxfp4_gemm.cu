@@ -1123,14 +1123,18 @@ MxGemmPlan plan_mx_gemm(const MxGemmShape& s, int pairs, int sms) {
   pl.tm = static_cast<int>((s.m + kPTile - 1) / kPTile);
   pl.tn = static_cast<int>((s.n + kPTile - 1) / kPTile);
   const int64_t tiles = s.count * pl.tm * pl.tn;
-  // Few tiles and a long K: split it. A stage takes a pair about 0.44 us, and
-  // the partial tiles with the kernel that adds them 5.5 us, so at least 14
-  // stages have to be saved (768 x 768, 9 tiles: K 4096 13.0 us unsplit
-  // against 13.3-14.9, K 8192 20.0 against 14.0).
+  // Few tiles and a long K: split it. A stage takes a pair about 0.29 us; the
+  // partial tiles and the kernel that adds them cost 3 us with one tile (4 MB
+  // of them) and 8 with 36 (19 MB), so 12 stages have to be saved, and one more
+  // for every two tiles. In us, unsplit against split: 200 x 200 (1 tile), K 3584
+  // 9.1 / 9.1, K 4096 9.7 / 9.3, K 8192 14.7 / 9.8; 768 x 768 (9), K 4096
+  // 11.5 / 11.6, K 5120 12.7 / 11.6, K 8192 16.2 / 12.8; 1000 x 1000 (16), K 6144
+  // 13.3 / 13.3, K 8192 15.6 / 14.1; 1500 x 1500 (36), K 8192 16.6 / 19.8,
+  // K 12288 21.2 / 22.7, K 16384 25.9 / 25.5.
   pl.split = 1;
   if (tiles * 2 <= pairs) {
     const int64_t sp = pairs / tiles < 16 ? pairs / tiles : 16;
-    if (kstages - (kstages + sp - 1) / sp >= 14) pl.split = static_cast<int>(sp);
+    if (2 * (kstages - (kstages + sp - 1) / sp) >= 24 + tiles) pl.split = static_cast<int>(sp);
   }
   pl.kc = (kstages + pl.split - 1) / pl.split;
   pl.split = (kstages + pl.kc - 1) / pl.kc;
