@@ -359,7 +359,7 @@ muon_status muon_mxfp4_matmul(const muon_mxfp4* a, const muon_mxfp4* b, const vo
   p.status = static_cast<int*>(ws);
   p.wait_limit_ns = static_cast<unsigned long long>(wait_limit_seconds() * 1e9);
   p.fault = fault_mode();
-  return launch_mx_gemm(p, pl, out_dtype == MUON_BF16, pairs, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess
+  return launch_mx_gemm(p, pl, out_dtype == MUON_BF16, pairs, static_cast<cudaStream_t>(stream)) == cudaSuccess
              ? MUON_OK
              : MUON_ERR_CUDA;
 }

@@ -311,7 +311,8 @@ __device__ __noinline__ void finish_stages(uint64_t* full, volatile GaveUp* reco
 // ------------------------------------------------------------------ pair kernel
 // How results leave: partial tiles of a split product, TMA stores (and addends by
 // TMA loads), or loads and stores of the epilogue warps where out's rows do not
-// start on 16-byte boundaries. One kernel each: together they spill registers.
+// start on 16-byte boundaries. One kernel each: together they spill registers
+// (apart, the one for partial tiles 36 bytes and the fp32 one by TMA 8).
 enum PairStore : int { kStoreParts = 0, kStoreTma = 1, kStoreTmaAdd = 2, kStorePlain = 3, kStoreAdd = 4 };
 
 template <bool kBf16, int kStore>
@@ -1096,10 +1097,13 @@ MxGemmPlan plan_mx_gemm(const MxGemmShape& s, int pairs, int sms) {
   MxGemmPlan pl{};
   const int kstages = static_cast<int>((s.k + 255) / 256);
   const int64_t small = s.m < s.n ? s.m : s.n, large = s.m < s.n ? s.n : s.m;
-  // Few rows on one side. Up to 32 the few-row kernel is faster everywhere (16 x
-  // 2560 x 2560: 6 against 10 us, 16 x 50304 x 768: 10 against 13); up to 64
-  // where the other side has few tiles too, so that K can be split over many
-  // CTAs (64 x 2560 x 2560: 8 against 10 us, but 64 x 10240 x 2560: 21 against 11).
+  // Few rows on one side. Few-row against pair kernel, in us: up to 32 rows 32 x
+  // 2560 x 2560 6.0 / 7.7, 16 x 50304 x 768 9.2 / 10.2, 32 x 10240 x 2560 8.9 /
+  // 9.1, 48 of 16 x 768 x 768 8.3 / 8.3, but 32 x 50304 x 768 10.6 / 10.3. Up to 64
+  // rows where the other side has few tiles too, so that K can be split over
+  // many CTAs: 64 x 2560 x 2560 7.4 / 8.4, 64 x 768 x 3200 6.7 / 8.7 (64 x 10240 x
+  // 2560 would be 12.9 / 9.3). At that limit and with a short K the pair kernel
+  // is a little faster: 64 x 4736 x 2560 9.0 / 8.6, 64 x 768 x 768 6.0 / 5.7.
   const int64_t tall = (large + kRows - 1) / kRows;
   if (small <= 32 || (small <= 64 && s.count * tall <= sms / 4)) {
     pl.few = true;
@@ -1193,7 +1197,7 @@ cudaError_t mx_gemm_prepare(int* max_pairs) {
 }
 
 cudaError_t launch_mx_gemm(const MxGemmParams& p, const MxGemmPlan& plan, bool bf16, int max_pairs,
-                           int sms, cudaStream_t s) {
+                           cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;

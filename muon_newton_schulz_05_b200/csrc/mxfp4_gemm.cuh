@@ -51,6 +51,6 @@ struct MxGemmPlan {
 MxGemmPlan plan_mx_gemm(const MxGemmShape& s, int pairs, int sms);
 cudaError_t mx_gemm_prepare(int* max_pairs);
 cudaError_t launch_mx_gemm(const MxGemmParams& p, const MxGemmPlan& plan, bool bf16, int max_pairs,
-                           int sms, cudaStream_t s);
+                           cudaStream_t s);
 
 }  // namespace muon
