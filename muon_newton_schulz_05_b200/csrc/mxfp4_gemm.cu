@@ -15,7 +15,10 @@
 // columns side by side, so the accumulators overlap by 96 columns (0..255 and
 // 160..415; scales above): the epilogue drains the shared columns of a tile
 // first, and the next tile's MMAs start as soon as it has. 16384 x 10240 x 2560
-// takes 166 us (5.2 PFLOP/s, under the board's power cap), K 8192 438 us (6.3).
+// takes 164-171 us in bursts of up to 50 ms (5.2 PFLOP/s) and 194-197 under
+// lasting load, when the board's power cap holds the clock at 1.2 GHz; K 8192
+// 448-468 (6.1) and 536-550. The tensor pipe is busy for 58 % of the cycles at
+// K 2560 and 79 % at K 8192; a tile costs 2600-2900 cycles without MMAs.
 // Products with few tiles and a long K are split along K into fp32 partial
 // tiles, which a second kernel adds in split order (deterministic).
 //
@@ -192,7 +195,7 @@ __device__ __forceinline__ void store_pair_tma(const MxGemmParams& p, uint8_t* b
 // lanes load and store neighbouring columns, four at a time where rows of bf16
 // have a multiple of 4 elements (in fp32 those go by TMA). The addends of 16
 // rows are on their way at once. (Rows that start anywhere: 4 x 1000 x 1537 x
-// 771 takes 12.5 us, 1536 columns by TMA 9.2.)
+// 771 takes 12.2-12.8 us, 1536 columns by TMA 9.1.)
 template <bool kBf16, bool kAdd>
 __device__ __forceinline__ void store_chunk(const MxGemmParams& p, uint8_t* buf, int lane, const uint32_t* r,
                                             long long base, int row, int col, bool vec) {

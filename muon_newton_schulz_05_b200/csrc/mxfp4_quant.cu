@@ -11,9 +11,13 @@
 // quantize: persistent blocks take 128 x 128 tiles, read each once (cp.async,
 // the next tiles in flight while one is coded) and write both orientations
 // from shared memory, each with its whole 512-byte scale tile. A thread codes
-// whole blocks, along a row or down a column. Dropout is applied in the row pass, which writes the masked values
-// back for the column pass; the blend of the parameters with their average is
-// formed while the tile is filled.
+// whole blocks, along a row or down a column. Dropout is applied in the row
+// pass, which writes the masked values back for the column pass; the blend of the
+// parameters with their average is formed while the tile is filled.
+//
+// Bound by instructions, at 58-66 % of the issue slots: 16384 x 2560 bf16 to both
+// orientations 24 us (its bytes 20), with dropout 47, stochastic 90; fp32 38 (33)
+// and 101. The blend of 768 x 50304 runs at the memory's rate, 44 us.
 #include "dtype_io.cuh"
 #include "lowbit.cuh"
 #include "philox.cuh"
